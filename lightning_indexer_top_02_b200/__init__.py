@@ -10,7 +10,9 @@ C-ABI names are mirrored one to one (``csa_indexer_topk``,
 ``csa_indexer_topk_ex``, ``csa_indexer_workspace_size``, ``csa_status_string``,
 ``csa_last_device_error``, ``csa_set_wait_limit``, ``csa_set_launch_events``,
 ``csa_version``);
-``indexer_topk`` is the same call on torch tensors.
+``indexer_topk`` is the same call on torch tensors.  The cache operators
+(rotary positions, paged cache append and read, attention over a 4-bit cache)
+are in ``cache.py`` and re-exported here.
 """
 from __future__ import annotations
 
@@ -41,7 +43,9 @@ EXPORTS = ("csa_indexer_topk", "csa_indexer_topk_ex", "csa_indexer_workspace_siz
            "csa_indexer_plan", "csa_indexer_topk_noalloc", "csa_sparse_attention",
            "csa_union_selections", "csa_merge_topk", "csa_merge_workspace_size",
            "csa_status_string", "csa_last_device_error", "csa_set_wait_limit",
-           "csa_set_launch_events", "csa_version")
+           "csa_set_launch_events", "csa_version", "csa_rope_frequencies", "csa_rotary",
+           "csa_cache_append", "csa_cache_read", "csa_cache_attention",
+           "csa_cache_attention_workspace_size")
 
 
 class CsaError(RuntimeError):
@@ -124,6 +128,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.csa_set_launch_events.restype = I
     lib.csa_version.argtypes = []
     lib.csa_version.restype = I
+    cache.declare(lib)
     _lib = lib
     return lib
 
@@ -327,3 +332,9 @@ def union_selections(idx_lists, T: int, cap: Optional[int] = None, stream=None):
     if st != CSA_OK:
         raise CsaError(st, "csa_union_selections")
     return out, count
+
+
+from . import cache  # noqa: E402
+from .cache import (Cache, cache_append, cache_attention, cache_read, csa_cache_append,  # noqa: E402,F401
+                    csa_cache_attention, csa_cache_attention_workspace_size, csa_cache_read,
+                    csa_rope_frequencies, csa_rotary, make_cache, rope_frequencies, rotary)

@@ -1,0 +1,598 @@
+// cache_attn_kernel.cuh -- attention over a cache held in 4 bits, few query
+// rows per cached row (csa_cache_attention, include/csa_cache.h).
+//
+// The query rows that share cached rows (all the queries and heads of one
+// cache head; with a selection, the heads of one query) go in tiles of 8 * kNT
+// rows, the N of mma.m16n8k16; the cached rows are its M:
+//   S^T [16 keys x 8 rows]  = K  [16 x Dk] . Q^T [Dk x 8]
+//   O^T [16 dims x 8 rows] += V^T [16 x 16 keys] . P^T [16 keys x 8]
+// With at most 16 rows the work is bound by reading the cache (9/16 byte an
+// element against 4 rows' flops an element), so what matters is how few
+// instructions stand between the load of a code and its use.  The codes go from
+// global memory straight into registers in the layout of the MMA's A operand:
+// no shared memory, no transposition.
+//   K: the contraction's order is free, so thread (g, t) of a warp takes the
+//     16 * NG consecutive elements 16 * NG * t.. of the rows of its two keys --
+//     whole scale groups, one wide load -- and the query fragments are laid
+//     out to match.
+//   V: a key's order in the tile is free too: thread (g, t) reads rows
+//     4t .. 4t+3 of 16 keys, elements VU * g.. of each; two keys' codes of one
+//     dimension are merged into a byte (one and-or for eight codes) that
+//     converts to the f16 pair that the A operand wants.
+//   P^T: the S^T accumulator holds (key g, rows 2t, 2t+1); movmatrix
+//     transposes the packed pairs into the B operand.
+// Values are exact in f16: an E2M1 code times an E4M3 scale has six
+// significant bits and lies within 2^-10 .. 2688 or is zero.  A query row is scaled by a
+// power of two to a largest magnitude in [1, 2): what bf16 holds down to
+// 2^-14 of it stays exact, smaller elements are off by at most 2^-25 of the largest.
+// P is f16 (11 bits), at most 2^8 where the running maximum lags; sums,
+// maxima and O are fp32.
+//
+// Tensor-core work here is mma.sync on purpose: tcgen05 reads operands from
+// shared memory, where writing the converted tile and reading it back would
+// move 4 bytes an element for each 9/16 byte that memory delivers, more than
+// shared memory's 128 bytes a clock allow at the memory's rate.
+//
+// Warps take blocks of 32 keys of a block's share of the keys in turn and
+// keep their own running maxima, sums and O; they are joined in shared
+// memory at the end, and the shares of one tile by a second kernel.
+#pragma once
+#include "cache_common.cuh"
+#include "ptx.cuh"
+
+namespace csa {
+namespace cattn {
+
+using cache::CacheView;
+using cache::FastDiv;
+using cache::PageMap;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kBlock = 32;                  // keys a warp takes at a time
+constexpr float kLag = 8.0f;                // the maximum is raised past 2^8 only
+constexpr int kNoKey = 0x7FFFFFFF;          // a position no query sees
+
+struct AttnParams {
+    const __nv_bfloat16 *q;                 // [B, S, HA, Dk]
+    CacheView ck, cv;
+    PageMap pm;
+    const int32_t *kv_len;
+    const int32_t *idx;                     // [B, S, topk] or null
+    int topk;
+    int B, S, HA, H, G;                     // G = HA / H
+    int causal;
+    float sl2;                              // scale * k tensor scale * log2(e)
+    float v_scale;
+    __nv_bfloat16 *out;
+    float *lse;
+    int splits;                             // shares of the keys
+    int tiles;                              // row tiles of a group
+    int rows;                               // query rows of a group: S * G, or G with idx
+    int capacity;                           // positions the page table reaches
+    float *part;                            // [work][split][rows of a tile][Dv + 2]
+};
+
+// The group of query rows that a work item belongs to.
+struct Group {
+    int b, h, i0;                           // sequence, cache head, first query
+    int r0;                                 // first row of the tile
+};
+
+__device__ __forceinline__ Group group_of(const AttnParams &p, int w, int tile_rows)
+{
+    Group g;
+    g.r0 = (w % p.tiles) * tile_rows;
+    w /= p.tiles;
+    g.h = w % p.H;
+    w /= p.H;
+    if (p.idx) {
+        g.i0 = w % p.S;
+        g.b = w / p.S;
+    } else {
+        g.i0 = 0;
+        g.b = w;
+    }
+    return g;
+}
+
+// Query and head of row r of a group.
+__device__ __forceinline__ void row_of(const AttnParams &p, const Group &g, int r, int &i, int &head)
+{
+    const int k = r / p.G;
+    i = g.i0 + k;
+    head = g.h * p.G + r - k * p.G;
+}
+
+// Positions below this are seen by query i (len > 0).
+__device__ __forceinline__ int seen(const AttnParams &p, int len, int i)
+{
+    return p.causal ? len - p.S + i + 1 : len;
+}
+
+template <int N> struct Bytes { uint32_t w[(N + 3) / 4]; };
+
+// N bytes from an address aligned to the largest power of two dividing N (at most 16).
+template <int N>
+__device__ __forceinline__ Bytes<N> load_bytes(const uint8_t *src)
+{
+    Bytes<N> r;
+    if constexpr (N % 16 == 0) {
+#pragma unroll
+        for (int j = 0; j < N / 16; ++j) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + j);
+            r.w[4 * j] = v.x;
+            r.w[4 * j + 1] = v.y;
+            r.w[4 * j + 2] = v.z;
+            r.w[4 * j + 3] = v.w;
+        }
+    } else if constexpr (N % 8 == 0) {
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src) + j);
+            r.w[2 * j] = v.x;
+            r.w[2 * j + 1] = v.y;
+        }
+    } else if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j)
+            r.w[j] = __ldg(reinterpret_cast<const uint32_t *>(src) + j);
+    } else if constexpr (N == 2) {
+        r.w[0] = __ldg(reinterpret_cast<const uint16_t *>(src));
+    } else {
+        static_assert(N < 4, "byte loads");
+        uint32_t v = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            v |= static_cast<uint32_t>(__ldg(src + j)) << (8 * j);
+        r.w[0] = v;
+    }
+    return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Byte j (constant after unrolling) of a packed word as an f16 pair.
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, int j)
+{
+    switch (j) {
+    case 0: return cache::f16x2_of_e2m1x2<0>(w);
+    case 1: return cache::f16x2_of_e2m1x2<1>(w);
+    case 2: return cache::f16x2_of_e2m1x2<2>(w);
+    default: return cache::f16x2_of_e2m1x2<3>(w);
+    }
+}
+
+template <int kDk, int kDv, int kNT>
+struct Shape {
+    static constexpr int NG = kDk / 64;                  // K: scale groups a thread takes of a row
+    static constexpr int VU = kDv % 128 == 0 ? 16 : 8;   // V: consecutive elements a thread takes
+    static constexpr int NU = kDv / (8 * VU);            // and how many times
+    static constexpr int MT = kDv / 16;                  // output m-tiles
+    static constexpr int kRows = 8 * kNT;
+    static constexpr int kSmem = kWarps * kRows * (kDv + 2) * 4;
+};
+
+// The raw codes and scales of 32 keys, as this thread uses them.
+template <class Sh>
+struct Raw {
+    Bytes<8 * Sh::NG> k[4];                              // rows of the keys g, g+8 of two tiles
+    Bytes<Sh::NG> ks[4];
+    Bytes<Sh::VU / 2> v[8][Sh::NU];                      // rows 4t .. 4t+3 of two tiles
+    uint8_t vs[8][Sh::NU];
+    int pos;                                             // lane's key: its position (kNoKey: none)
+};
+
+// Position, page and row of the key in slot `slot` of a group.
+__device__ __forceinline__ void find_key(const AttnParams &p, const int32_t *list, const int32_t *table,
+                                         int slot, int last, int limit, int &pos, int &page, int &off)
+{
+    pos = kNoKey;
+    page = off = 0;
+    if (slot < last) {
+        const int s = list ? __ldg(list + slot) : slot;
+        if (s >= 0 && s < limit && p.pm.locate(table, s, page, off))
+            pos = s;
+        else
+            page = off = 0;
+    }
+}
+
+template <int kDk, int kDv, int kNT>
+__global__ void __launch_bounds__(kThreads, kNT == 1 && kDk + kDv <= 256 ? 3 : 2)
+    cache_attn_kernel(const AttnParams p)
+{
+    using Sh = Shape<kDk, kDv, kNT>;
+    constexpr int NG = Sh::NG, VU = Sh::VU, NU = Sh::NU, MT = Sh::MT, RT = Sh::kRows;
+    extern __shared__ float smem[];                      // [warp][row][Dv + 2]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int work = blockIdx.x / p.splits, split = blockIdx.x - work * p.splits;
+    const Group gr = group_of(p, work, RT);
+    const int len = __ldg(p.kv_len + gr.b);
+    const int32_t *table = p.pm.table + gr.b * p.pm.table_stride;
+    const int32_t *list = p.idx ? p.idx + (static_cast<long long>(gr.b) * p.S + gr.i0) * p.topk : nullptr;
+
+    // the tile's rows: what the last and the first of them see
+    const int r_last = min(gr.r0 + RT, p.rows) - 1;
+    const int see_hi = len > 0 ? seen(p, len, gr.i0 + r_last / p.G) : 0;
+    const int see_lo = len > 0 ? seen(p, len, gr.i0 + gr.r0 / p.G) : 0;
+    const int slots = p.idx ? (see_hi > 0 ? p.topk : 0) : min(max(see_hi, 0), p.capacity);
+    const int blocks = (slots + kBlock - 1) / kBlock;
+    const int b_lo = static_cast<int>(static_cast<long long>(blocks) * split / p.splits);
+    const int b_hi = static_cast<int>(static_cast<long long>(blocks) * (split + 1) / p.splits);
+
+    // query fragments: row g of each n-tile, elements 16 NG t.., scaled by a power of two
+    uint32_t qf[kNT][4 * NG][2];
+    float f[kNT][2];                                     // factor of rows 2t, 2t+1 (log2 domain)
+    int lim[kNT][2];                                     // and the positions they see
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+        const int r = gr.r0 + 8 * n + g;
+        float x[16 * NG];
+        float peak = 0.0f;
+        int i = 0, head = 0;
+        if (r < p.rows) {
+            row_of(p, gr, r, i, head);
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                p.q + ((static_cast<long long>(gr.b) * p.S + i) * p.HA + head) * kDk + 16 * NG * t);
+#pragma unroll
+            for (int j = 0; j < 2 * NG; ++j) {
+                const uint4 w = __ldg(src + j);
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = cache::float2_of_bf16x2(u[e]);
+                    x[8 * j + 2 * e] = v.x;
+                    x[8 * j + 2 * e + 1] = v.y;
+                    peak = fmaxf(peak, fmaxf(fabsf(v.x), fabsf(v.y)));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16 * NG; ++j)
+                x[j] = 0.0f;
+        }
+        peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
+        peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
+        // exponents of the scale and of its inverse, both normal powers of two
+        const int e = min(max(static_cast<int>(__float_as_uint(peak) >> 23), 1), 253);
+        const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+#pragma unroll
+        for (int s = 0; s < 4 * NG; ++s) {
+            qf[n][s][0] = f16x2_of(x[4 * s] * down, x[4 * s + 1] * down);
+            qf[n][s][1] = f16x2_of(x[4 * s + 2] * down, x[4 * s + 3] * down);
+        }
+        const float fr = up * p.sl2;
+        const int see = r < p.rows && len > 0 ? seen(p, len, i) : 0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            f[n][c] = __shfl_sync(0xffffffffu, fr, 4 * (2 * t + c));
+            lim[n][c] = __shfl_sync(0xffffffffu, see, 4 * (2 * t + c));
+        }
+    }
+
+    float o[MT][kNT][4];
+    float m[kNT][2], l[kNT][2];
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                o[j][n][c] = 0.0f;
+    }
+
+    // rows of a tile of 16 keys: K rows k0, k0 + 2 (MMA rows g, g + 8), V rows 4t ..
+    const int k0 = 4 * (g >> 1) + (g & 1);
+    auto load = [&](int block, Raw<Sh> &raw) {
+        int page, off;
+        find_key(p, list, table, block * kBlock + lane, slots, see_hi, raw.pos, page, off);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 16 * (j >> 1) + k0 + 2 * (j & 1);
+            const int pg = __shfl_sync(0xffffffffu, page, r), of = __shfl_sync(0xffffffffu, off, r);
+            raw.k[j] = load_bytes<8 * NG>(cache::row_data(p.ck, p.pm, pg, gr.h, of) + 8 * NG * t);
+            raw.ks[j] = load_bytes<NG>(cache::row_scale(p.ck, p.pm, pg, gr.h, of) + NG * t);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = 16 * (j >> 2) + 4 * t + (j & 3);
+            const int pg = __shfl_sync(0xffffffffu, page, r), of = __shfl_sync(0xffffffffu, off, r);
+            const int ok = __shfl_sync(0xffffffffu, raw.pos, r) != kNoKey;
+            const uint8_t *vd = cache::row_data(p.cv, p.pm, pg, gr.h, of) + (VU / 2) * g;
+            const uint8_t *vc = cache::row_scale(p.cv, p.pm, pg, gr.h, of) + (VU * g) / 16;
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                raw.v[j][u] = load_bytes<VU / 2>(vd + 4 * VU * u);
+                // a masked key's scale may be anything, NaN too: its P is zero, so its V is made zero
+                raw.vs[j][u] = ok ? __ldg(vc + (VU / 2) * u) : 0;
+            }
+        }
+    };
+
+    Raw<Sh> raw;
+    int blk = b_lo + warp;
+    if (blk < b_hi)
+        load(blk, raw);
+    while (blk < b_hi) {
+        const Raw<Sh> cur = raw;
+        const int next = blk + kWarps;
+        if (next < b_hi)
+            load(next, raw);
+        // S^T of two tiles of 16 keys
+        float s[2][kNT][4];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    s[a][n][c] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NG; ++c) {
+                // the group's scale in both halves
+                uint32_t sc[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t byte = cur.ks[2 * a + e].w[0] >> (8 * c) & 0xFFu;
+                    sc[e] = cache::f16x2_of_e4m3x2(byte * 0x0101u);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t w0 = cur.k[2 * a].w[2 * c + (q >> 1)];
+                    const uint32_t w1 = cur.k[2 * a + 1].w[2 * c + (q >> 1)];
+                    const int j = 2 * (q & 1);
+                    const uint32_t a0 = hmul2(pair_of(w0, j), sc[0]), a2 = hmul2(pair_of(w0, j + 1), sc[0]);
+                    const uint32_t a1 = hmul2(pair_of(w1, j), sc[1]), a3 = hmul2(pair_of(w1, j + 1), sc[1]);
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n)
+                        mma16816(s[a][n], a0, a1, a2, a3, qf[n][4 * c + q][0], qf[n][4 * c + q][1]);
+                }
+            }
+        }
+        // masks: the positions of the thread's four keys
+        const bool whole = __all_sync(0xffffffffu, cur.pos < see_lo);
+        int kp[2][2];
+        if (!whole) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    kp[a][e] = __shfl_sync(0xffffffffu, cur.pos, 16 * a + k0 + 2 * e);
+        }
+        bool raise = false;
+        float top[kNT][2];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float best = -INFINITY;
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = s[a][n][2 * e + c] * f[n][c];
+                        if (!whole && kp[a][e] >= lim[n][c])
+                            x = -INFINITY;
+                        s[a][n][2 * e + c] = x;
+                        best = fmaxf(best, x);
+                    }
+                top[n][c] = best;
+                raise = raise || best > m[n][c] + kLag;   // (-inf > -inf is false)
+            }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float best = top[n][c];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1)
+                        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
+                    if (best > m[n][c]) {
+                        const float a = ex2_approx(m[n][c] - best);   // first keys: 2^-inf = 0
+                        m[n][c] = best;
+                        l[n][c] *= a;
+#pragma unroll
+                        for (int j = 0; j < MT; ++j) {
+                            o[j][n][c] *= a;
+                            o[j][n][2 + c] *= a;
+                        }
+                    }
+                }
+        }
+        // P, its sums, and P^T as the B operand
+        uint32_t pb[2][kNT][2];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+            const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0];
+            const float m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float p0 = ex2_approx(s[a][n][2 * e] - m0);
+                    const float p1 = ex2_approx(s[a][n][2 * e + 1] - m1);
+                    l[n][0] += p0;
+                    l[n][1] += p1;
+                    pb[a][n][e] = transpose8x8(f16x2_of(p0, p1));
+                }
+        }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                uint32_t sc[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    sc[e] = cache::f16x2_of_e4m3x2(cur.vs[4 * a + 2 * e][u] | cur.vs[4 * a + 2 * e + 1][u] << 8);
+#pragma unroll
+                for (int w = 0; w < VU / 8; ++w) {
+                    uint32_t lo[2], hi[2];              // even and odd dimensions, a byte = two keys
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t x = cur.v[4 * a + 2 * e][u].w[w], y = cur.v[4 * a + 2 * e + 1][u].w[w];
+                        lo[e] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
+                        hi[e] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t a0 = hmul2(pair_of(lo[0], j), sc[0]), a1 = hmul2(pair_of(hi[0], j), sc[0]);
+                        const uint32_t a2 = hmul2(pair_of(lo[1], j), sc[1]), a3 = hmul2(pair_of(hi[1], j), sc[1]);
+#pragma unroll
+                        for (int n = 0; n < kNT; ++n)
+                            mma16816(o[(VU / 2) * u + 4 * w + j][n], a0, a1, a2, a3, pb[a][n][0], pb[a][n][1]);
+                    }
+                }
+            }
+        blk = next;
+    }
+
+    // join the warps: every warp's O, maxima and sums go to shared memory
+    float *mine = smem + warp * RT * (kDv + 2);
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float sum = l[n][c];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            float *row = mine + (8 * n + 2 * t + c) * (kDv + 2);
+            if (g == 0) {
+                row[kDv] = m[n][c];
+                row[kDv + 1] = sum;
+            }
+            // m-tile j of unit u: rows g, g + 8 are dimensions 8 VU u + VU g + 2j, + 1
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const int d = 8 * VU * (j / (VU / 2)) + VU * g + 2 * (j % (VU / 2));
+                *reinterpret_cast<float2 *>(row + d) = make_float2(o[j][n][c], o[j][n][2 + c]);
+            }
+        }
+    __syncthreads();
+    for (int r = warp; r < RT && gr.r0 + r < p.rows; r += kWarps) {
+        const float *row = smem + r * (kDv + 2);
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            top = fmaxf(top, row[w * RT * (kDv + 2) + kDv]);
+        float a[kWarps], sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float *wr = row + w * RT * (kDv + 2);
+            a[w] = top == -INFINITY ? 0.0f : ex2_approx(wr[kDv] - top);
+            sum += a[w] * wr[kDv + 1];
+        }
+        if (p.splits > 1) {
+            float *dst = p.part + (static_cast<long long>(blockIdx.x) * RT + r) * (kDv + 2);
+            for (int d = lane; d < kDv; d += 32) {
+                float x = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    x += a[w] * row[w * RT * (kDv + 2) + d];
+                dst[d] = x;
+            }
+            if (lane == 0) {
+                dst[kDv] = top;
+                dst[kDv + 1] = sum;
+            }
+            continue;
+        }
+        int i, head;
+        row_of(p, gr, gr.r0 + r, i, head);
+        const long long at = (static_cast<long long>(gr.b) * p.S + i) * p.HA + head;
+        const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
+        for (int d = lane; d < kDv; d += 32) {
+            float x = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                x += a[w] * row[w * RT * (kDv + 2) + d];
+            p.out[at * kDv + d] = __float2bfloat16_rn(x * inv);
+        }
+        if (p.lse && lane == 0)
+            p.lse[at] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
+// Joins the shares of one row: out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
+// One warp a row.
+__global__ void __launch_bounds__(128) cache_attn_join_kernel(const AttnParams p, int Dv, int tile_rows,
+                                                              long long rows)
+{
+    const int lane = threadIdx.x & 31;
+    const long long at = blockIdx.x * 4ll + (threadIdx.x >> 5);   // (b, i, head)
+    if (at >= rows)
+        return;
+    const int head = static_cast<int>(at % p.HA);
+    const long long bi = at / p.HA;
+    const int h = head / p.G;
+    const int r = p.idx ? head - h * p.G : static_cast<int>(bi % p.S) * p.G + head - h * p.G;
+    const long long group = p.idx ? bi * p.H + h : bi / p.S * p.H + h;
+    const long long work = group * p.tiles + r / tile_rows;
+    const long long stride = static_cast<long long>(tile_rows) * (Dv + 2);
+    const float *src = p.part + work * p.splits * stride + (r % tile_rows) * (Dv + 2);
+    float top = -INFINITY;
+    for (int s = lane; s < p.splits; s += 32)
+        top = fmaxf(top, src[s * stride + Dv]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float sum = 0.0f;
+    if (top != -INFINITY)
+        for (int s = lane; s < p.splits; s += 32)
+            sum += ex2_approx(src[s * stride + Dv] - top) * src[s * stride + Dv + 1];
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
+    for (int d = 2 * lane; d < Dv; d += 64) {
+        float x = 0.0f, y = 0.0f;
+        if (top != -INFINITY)
+            for (int s = 0; s < p.splits; ++s) {
+                const float a = ex2_approx(src[s * stride + Dv] - top);
+                const float2 v = *reinterpret_cast<const float2 *>(src + s * stride + d);
+                x += a * v.x;
+                y += a * v.y;
+            }
+        *reinterpret_cast<uint32_t *>(p.out + at * Dv + d) = cache::bf16x2_of(x * inv, y * inv);
+    }
+    if (p.lse && lane == 0)
+        p.lse[at] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+} // namespace cattn
+} // namespace csa

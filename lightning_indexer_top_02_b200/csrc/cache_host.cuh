@@ -1,0 +1,581 @@
+// cache_host.cuh -- host side of the cache operators (include/csa_cache.h):
+// validation, launch shapes, the C ABI.  Included once, by csa_indexer.cu.
+#pragma once
+#include <cmath>
+
+#include "csa_cache.h"
+#include "cache_attn_kernel.cuh"
+#include "cache_rows_kernel.cuh"
+#include "rotary_kernel.cuh"
+
+namespace {
+
+using csa::cache::CacheView;
+using csa::cache::FastDiv;
+using csa::cache::PageMap;
+
+constexpr long long kIntLimit = (1ll << 31) - 64;
+
+// Bytes of a row's data and of its scales.
+long long cache_row_bytes(const csa_cache_t &c)
+{
+    return c.dtype == CSA_CACHE_BF16 ? 2ll * c.D : c.dtype == CSA_CACHE_E4M3 ? c.D : c.D / 2;
+}
+
+long long cache_scale_bytes(const csa_cache_t &c)
+{
+    return c.dtype == CSA_CACHE_BF16 ? 0 : c.dtype == CSA_CACHE_E4M3 ? 4 : c.D / 16;
+}
+
+csa_status_t validate_cache(const csa_cache_t &c)
+{
+    if (c.dtype < CSA_CACHE_BF16 || c.dtype > CSA_CACHE_E2M1 || c.H <= 0 || c.D <= 0 ||
+        c.num_pages <= 0 || c.page_size <= 0 || c.page_stride < 0 || c.scale_page_stride < 0)
+        return CSA_ERR_INVALID_ARG;
+    if (c.D % 16 != 0 || c.D > 512 ||
+        static_cast<long long>(c.H) * c.page_size >= kIntLimit)
+        return CSA_ERR_UNSUPPORTED;
+    const bool scaled = c.dtype != CSA_CACHE_BF16;
+    if (!c.data || !aligned(c.data, 16) || (scaled && (!c.scale || !aligned(c.scale, 16))))
+        return CSA_ERR_INVALID_ARG;
+    const long long rows = static_cast<long long>(c.H) * c.page_size;
+    if (c.page_stride && (c.page_stride % 16 != 0 || c.page_stride < rows * cache_row_bytes(c)))
+        return CSA_ERR_INVALID_ARG;
+    if (scaled && c.scale_page_stride &&
+        (c.scale_page_stride % cache_scale_bytes(c) != 0 ||
+         c.scale_page_stride < rows * cache_scale_bytes(c)))
+        return CSA_ERR_INVALID_ARG;
+    // a row's data must start on 16 bytes: dense pages of E2M1 rows of 8 (mod 16) bytes do not
+    if (cache_row_bytes(c) % 16 != 0)
+        return CSA_ERR_UNSUPPORTED;
+    if (c.dtype == CSA_CACHE_E2M1 && !(c.tensor_scale > 0.0f && std::isfinite(c.tensor_scale)))
+        return CSA_ERR_INVALID_ARG;
+    return CSA_OK;
+}
+
+csa_status_t validate_pages(const int32_t *kv_len, const int32_t *table, int max_pages,
+                            long long table_stride, int page_size)
+{
+    if (max_pages <= 0 || table_stride < max_pages)
+        return CSA_ERR_INVALID_ARG;
+    if (!kv_len || !table || !aligned(kv_len, 4) || !aligned(table, 4))
+        return CSA_ERR_INVALID_ARG;
+    if (static_cast<long long>(max_pages) * page_size >= kIntLimit)
+        return CSA_ERR_UNSUPPORTED;
+    return CSA_OK;
+}
+
+CacheView cache_view(const csa_cache_t &c)
+{
+    const long long rows = static_cast<long long>(c.H) * c.page_size;
+    CacheView v;
+    v.data = static_cast<uint8_t *>(c.data);
+    v.scale = static_cast<uint8_t *>(c.scale);
+    v.row_bytes = static_cast<int>(cache_row_bytes(c));
+    v.scale_bytes = static_cast<int>(cache_scale_bytes(c));
+    v.page_stride = c.page_stride ? c.page_stride : rows * v.row_bytes;
+    v.scale_stride = c.scale_page_stride ? c.scale_page_stride : rows * v.scale_bytes;
+    v.tensor_scale = c.dtype == CSA_CACHE_E2M1 ? c.tensor_scale : 1.0f;
+    return v;
+}
+
+PageMap page_map(const csa_cache_t &c, const int32_t *table, int max_pages, long long table_stride)
+{
+    PageMap pm;
+    pm.table = table;
+    pm.table_stride = table_stride;
+    pm.max_pages = max_pages;
+    pm.num_pages = c.num_pages;
+    pm.page_size = c.page_size;
+    pm.div = FastDiv::of(static_cast<uint32_t>(c.page_size));
+    return pm;
+}
+
+bool same_pages(const csa_cache_t &a, const csa_cache_t &b)
+{
+    return a.dtype == b.dtype && a.H == b.H && a.num_pages == b.num_pages && a.page_size == b.page_size;
+}
+
+csa_status_t launched() { return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
+
+} // namespace
+
+// ---------------------------------------------------------------------------
+// Rotation frequencies (host).
+extern "C" csa_status_t csa_rope_frequencies(int rot_dim, double base, int scaling, double factor,
+                                             int original_len, double beta_fast, double beta_slow,
+                                             float *inv_freq, float *scale)
+{
+    const double pi = 3.14159265358979323846;
+    if (rot_dim < 2 || rot_dim % 2 != 0 || !(base > 1.0) || !std::isfinite(base) || !inv_freq ||
+        !scale || scaling < CSA_ROPE_PLAIN || scaling > CSA_ROPE_YARN)
+        return CSA_ERR_INVALID_ARG;
+    if (scaling != CSA_ROPE_PLAIN && !(factor >= 1.0 && std::isfinite(factor)))
+        return CSA_ERR_INVALID_ARG;
+    if (scaling == CSA_ROPE_NTK && rot_dim == 2)
+        return CSA_ERR_INVALID_ARG;
+    double lo = 0.0, hi = 0.0;
+    if (scaling == CSA_ROPE_YARN) {
+        if (original_len <= 0 || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) || !std::isfinite(beta_fast))
+            return CSA_ERR_INVALID_ARG;
+        // the dimension (in pairs) that turns `turns` times within original_len
+        auto pair_of_turns = [&](double turns) {
+            return rot_dim * std::log(original_len / (turns * 2.0 * pi)) / (2.0 * std::log(base));
+        };
+        lo = std::fmax(std::floor(pair_of_turns(beta_fast)), 0.0);
+        hi = std::fmin(std::ceil(pair_of_turns(beta_slow)), rot_dim - 1.0);
+    }
+    if (scaling == CSA_ROPE_NTK)
+        base *= std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot_dim);
+        if (scaling == CSA_ROPE_LINEAR)
+            f /= factor;
+        if (scaling == CSA_ROPE_YARN) {
+            const double ramp = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3), 0.0), 1.0);
+            f = f / factor * ramp + f * (1.0 - ramp);
+        }
+        inv_freq[i] = static_cast<float>(f);
+    }
+    *scale = scaling == CSA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return CSA_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Rotary positions.
+namespace {
+
+using csa::rotary::RotaryParams;
+using RotaryFn = void (*)(const RotaryParams);
+
+template <typename T, int V>
+RotaryFn rotary_fn(bool inter)
+{
+    return inter ? csa::rotary::rotary_kernel<T, V, true> : csa::rotary::rotary_kernel<T, V, false>;
+}
+
+// Position of a head's other elements and the strides allow V elements at a time.
+bool rotary_fits(const csa_rotary_args_t *a, int v)
+{
+    const int unit = a->interleaved ? a->rot_dim : a->rot_dim / 2;
+    return unit % v == 0 && a->rot_offset % v == 0 && a->D % v == 0 && a->x_token_stride % v == 0 &&
+           a->x_head_stride % v == 0 && a->out_token_stride % v == 0 && a->out_head_stride % v == 0 &&
+           aligned(a->x, 16) && aligned(a->out, 16);
+}
+
+} // namespace
+
+extern "C" csa_status_t csa_rotary(const csa_rotary_args_t *args, cudaStream_t stream)
+{
+    NvtxRange range("csa_rotary");
+    const csa_rotary_args_t *a = args;
+    if (!a || a->N < 0 || a->H <= 0 || a->D <= 0 || a->dtype < CSA_ELEM_BF16 || a->dtype > CSA_ELEM_FP32 ||
+        a->rot_dim < 2 || a->rot_dim % 2 != 0 || a->rot_offset < 0 || a->rot_offset % 2 != 0 ||
+        a->rot_offset > a->D - a->rot_dim || !std::isfinite(a->scale))
+        return CSA_ERR_INVALID_ARG;
+    if (a->D > 1024 || static_cast<long long>(a->H) * a->D >= kIntLimit / 64)
+        return CSA_ERR_UNSUPPORTED;
+    if (a->N == 0)
+        return CSA_OK;
+    const int size = a->dtype == CSA_ELEM_FP32 ? 4 : 2;
+    if (!a->x || !a->out || !a->positions || !a->inv_freq || !aligned(a->x, size) ||
+        !aligned(a->out, size) || !aligned(a->positions, 4) || !aligned(a->inv_freq, 4))
+        return CSA_ERR_INVALID_ARG;
+    // rows of out may not overlap: heads within a token or tokens within a head, whichever is outer
+    const long long oh = a->out_head_stride, ot = a->out_token_stride;
+    if (a->x_head_stride < 0 || a->x_token_stride < 0 || oh < 0 || ot < 0 ||
+        (a->H > 1 && oh < a->D) || (a->N > 1 && ot < a->D) ||
+        (a->H > 1 && a->N > 1 && ot < (a->H - 1) * oh + a->D && oh < (a->N - 1) * ot + a->D))
+        return CSA_ERR_INVALID_ARG;
+    if (a->x == a->out && ((a->H > 1 && a->x_head_stride != oh) || (a->N > 1 && a->x_token_stride != ot)))
+        return CSA_ERR_INVALID_ARG;
+    const int sms = device_sms();
+    if (sms <= 0)
+        return CSA_ERR_CUDA;
+    RotaryParams p;
+    std::memset(&p, 0, sizeof p);
+    p.x = a->x;
+    p.out = a->out;
+    p.N = a->N;
+    p.H = a->H;
+    p.D = a->D;
+    p.xt = a->x_token_stride;
+    p.xh = a->x_head_stride;
+    p.ot = ot;
+    p.oh = oh;
+    p.positions = a->positions;
+    p.inv_freq = a->inv_freq;
+    p.half = a->rot_dim / 2;
+    p.off = a->rot_offset;
+    p.inverse = a->inverse != 0;
+    p.scale = a->scale;
+    p.copy = a->x != a->out;
+    const bool inter = a->interleaved != 0;
+    const int wide = 16 / size;
+    const int v = rotary_fits(a, wide) ? wide : 1;
+    p.pair_units = inter ? (v > 1 ? a->rot_dim / v : p.half) : p.half / v;
+    p.units = p.pair_units + (p.copy ? (a->D - a->rot_dim) / v : 0);
+    p.div_units = FastDiv::of(p.units);
+    // blocks: about eight units a thread; a token's heads are shared out when
+    // there are too few tokens to fill the GPU
+    const long long per_token = static_cast<long long>(a->H) * p.units;
+    const long long want = 8ll * csa::rotary::kThreads;
+    long long tokens = per_token >= want ? 1 : want / per_token;
+    while (tokens > 1 && (a->N + tokens - 1) / tokens < 4ll * sms)
+        tokens = (tokens + 1) / 2;
+    const long long most = 32768 / (8ll * p.half);       // cos and sin in 32 KB
+    p.tokens = static_cast<int>(tokens < most ? tokens : most);
+    const long long blocks = (a->N + p.tokens - 1) / p.tokens;
+    long long shares = (2ll * sms + blocks - 1) / blocks;
+    const long long most_shares = (per_token * p.tokens + csa::rotary::kThreads - 1) / csa::rotary::kThreads;
+    shares = shares < most_shares ? shares : most_shares;
+    shares = shares < 1 ? 1 : shares > a->H ? a->H : shares;
+    p.heads = static_cast<int>((a->H + shares - 1) / shares);
+    p.div_heads = FastDiv::of(p.heads);
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((a->H + p.heads - 1) / p.heads));
+    if (grid.y > 65535)
+        return CSA_ERR_UNSUPPORTED;
+    RotaryFn fn;
+    if (a->dtype == CSA_ELEM_FP32)
+        fn = v > 1 ? rotary_fn<float, 4>(inter) : rotary_fn<float, 1>(inter);
+    else if (a->dtype == CSA_ELEM_FP16)
+        fn = v > 1 ? rotary_fn<__half, 8>(inter) : rotary_fn<__half, 1>(inter);
+    else
+        fn = v > 1 ? rotary_fn<__nv_bfloat16, 8>(inter) : rotary_fn<__nv_bfloat16, 1>(inter);
+    if (!mark(0, stream))
+        return CSA_ERR_CUDA;
+    fn<<<grid, csa::rotary::kThreads, p.tokens * p.half * sizeof(float2), stream>>>(p);
+    const csa_status_t st = launched();
+    return st == CSA_OK && !mark(1, stream) ? CSA_ERR_CUDA : st;
+}
+
+// ---------------------------------------------------------------------------
+// Appending to and reading from a cache.
+namespace {
+
+int row_lanes(int D) { return pow2_ceil(D / 16); }
+
+template <int kType>
+void launch_append(const csa::cache::AppendParams &p, bool inter, unsigned grid, size_t smem,
+                   cudaStream_t stream)
+{
+    if (inter)
+        csa::cache::append_kernel<kType, true><<<grid, csa::cache::kRowThreads, smem, stream>>>(p);
+    else
+        csa::cache::append_kernel<kType, false><<<grid, csa::cache::kRowThreads, smem, stream>>>(p);
+}
+
+} // namespace
+
+extern "C" csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStream_t stream)
+{
+    NvtxRange range("csa_cache_append");
+    const csa_append_args_t *a = args;
+    if (!a || a->N < 0 || a->B < 0 || (!a->cu_tokens && (a->S < 0 || a->N != static_cast<long long>(a->B) * a->S)))
+        return CSA_ERR_INVALID_ARG;
+    csa_status_t st = validate_cache(a->cache_k);
+    if (st == CSA_OK && a->v)
+        st = validate_cache(a->cache_v);
+    if (st != CSA_OK)
+        return st;
+    if (a->v && !same_pages(a->cache_k, a->cache_v))
+        return CSA_ERR_INVALID_ARG;
+    if (a->inv_freq && (a->rot_dim < 2 || a->rot_dim % 2 != 0 || a->rot_offset < 0 || a->rot_offset % 2 != 0 ||
+                        a->rot_offset > a->cache_k.D - a->rot_dim || !std::isfinite(a->rope_scale) ||
+                        !aligned(a->inv_freq, 4)))
+        return CSA_ERR_INVALID_ARG;
+    if (a->N == 0 || a->B == 0)
+        return CSA_OK;
+    st = validate_pages(a->kv_len, a->page_table, a->max_pages, a->table_stride, a->cache_k.page_size);
+    if (st != CSA_OK)
+        return st;
+    if (!a->k || !aligned(a->k, 16) || (a->v && !aligned(a->v, 16)) || !aligned(a->cu_tokens, 4) ||
+        !aligned(a->positions, 4))
+        return CSA_ERR_INVALID_ARG;
+    if (a->k_token_stride < 0 || a->k_head_stride < 0 || a->k_token_stride % 8 != 0 || a->k_head_stride % 8 != 0 ||
+        (a->v && (a->v_token_stride < 0 || a->v_head_stride < 0 || a->v_token_stride % 8 != 0 ||
+                  a->v_head_stride % 8 != 0)))
+        return CSA_ERR_INVALID_ARG;
+    const int sms = device_sms();
+    if (sms <= 0)
+        return CSA_ERR_CUDA;
+    csa::cache::AppendParams p;
+    std::memset(&p, 0, sizeof p);
+    p.k = static_cast<const __nv_bfloat16 *>(a->k);
+    p.v = static_cast<const __nv_bfloat16 *>(a->v);
+    p.kt = a->k_token_stride;
+    p.kh = a->k_head_stride;
+    p.vt = a->v_token_stride;
+    p.vh = a->v_head_stride;
+    p.N = a->N;
+    p.B = a->B;
+    p.S = a->S;
+    p.H = a->cache_k.H;
+    p.Dk = a->cache_k.D;
+    p.Dv = a->v ? a->cache_v.D : 0;
+    p.cu = a->cu_tokens;
+    p.kv_len = a->kv_len;
+    p.pm = page_map(a->cache_k, a->page_table, a->max_pages, a->table_stride);
+    p.ck = cache_view(a->cache_k);
+    if (a->v)
+        p.cv = cache_view(a->cache_v);
+    p.inv_freq = a->inv_freq;
+    p.positions = a->positions;
+    p.half = a->inv_freq ? a->rot_dim / 2 : 0;
+    p.off = a->rot_offset;
+    p.rope_scale = a->rope_scale;
+    p.lanes_k = row_lanes(p.Dk);
+    p.lanes_v = a->v ? row_lanes(p.Dv) : 1;
+    // tokens a block takes: about four rounds of rows, fewer while blocks are few
+    int tokens = 4 * csa::cache::kRowThreads / (p.lanes_k * p.H);
+    tokens = tokens < 1 ? 1 : tokens > csa::cache::kMaxTile ? csa::cache::kMaxTile : tokens;
+    while (tokens > 1 && (a->N + tokens - 1) / tokens < 4 * sms)
+        tokens = (tokens + 1) / 2;
+    if (p.half && tokens > 2048 / p.half)                // cos and sin in 32 KB
+        tokens = 2048 / p.half;
+    p.tokens = tokens;
+    const unsigned grid = static_cast<unsigned>((static_cast<long long>(a->N) + tokens - 1) / tokens);
+    const size_t smem = static_cast<size_t>(tokens) * p.half * sizeof(csa::cache::Turn);
+    const bool inter = a->interleaved != 0;
+    if (!mark(0, stream))
+        return CSA_ERR_CUDA;
+    if (a->cache_k.dtype == CSA_CACHE_BF16)
+        launch_append<0>(p, inter, grid, smem, stream);
+    else if (a->cache_k.dtype == CSA_CACHE_E4M3)
+        launch_append<1>(p, inter, grid, smem, stream);
+    else
+        launch_append<2>(p, inter, grid, smem, stream);
+    st = launched();
+    return st == CSA_OK && !mark(1, stream) ? CSA_ERR_CUDA : st;
+}
+
+extern "C" csa_status_t csa_cache_read(const csa_cache_read_args_t *args, cudaStream_t stream)
+{
+    NvtxRange range("csa_cache_read");
+    const csa_cache_read_args_t *a = args;
+    if (!a || a->B < 0 || a->T < 0)
+        return CSA_ERR_INVALID_ARG;
+    csa_status_t st = validate_cache(a->cache);
+    if (st != CSA_OK)
+        return st;
+    if (a->B == 0 || a->T == 0)
+        return CSA_OK;
+    st = validate_pages(a->kv_len, a->page_table, a->max_pages, a->table_stride, a->cache.page_size);
+    if (st != CSA_OK)
+        return st;
+    if (!a->out || !aligned(a->out, 16))
+        return CSA_ERR_INVALID_ARG;
+    if (a->T >= kIntLimit)
+        return CSA_ERR_UNSUPPORTED;
+    const int sms = device_sms();
+    if (sms <= 0)
+        return CSA_ERR_CUDA;
+    csa::cache::ReadParams p;
+    std::memset(&p, 0, sizeof p);
+    p.c = cache_view(a->cache);
+    p.pm = page_map(a->cache, a->page_table, a->max_pages, a->table_stride);
+    p.kv_len = a->kv_len;
+    p.B = a->B;
+    p.T = a->T;
+    p.H = a->cache.H;
+    p.D = a->cache.D;
+    p.lanes = row_lanes(p.D);
+    p.rows = static_cast<long long>(a->B) * a->T * p.H;
+    p.out = static_cast<__nv_bfloat16 *>(a->out);
+    const int per = csa::cache::kRowThreads / p.lanes;
+    const long long need = (p.rows + per - 1) / per, most = 64ll * sms;
+    const unsigned grid = static_cast<unsigned>(need < most ? need : most);
+    if (!mark(0, stream))
+        return CSA_ERR_CUDA;
+    if (a->cache.dtype == CSA_CACHE_BF16)
+        csa::cache::read_kernel<0><<<grid, csa::cache::kRowThreads, 0, stream>>>(p);
+    else if (a->cache.dtype == CSA_CACHE_E4M3)
+        csa::cache::read_kernel<1><<<grid, csa::cache::kRowThreads, 0, stream>>>(p);
+    else
+        csa::cache::read_kernel<2><<<grid, csa::cache::kRowThreads, 0, stream>>>(p);
+    st = launched();
+    return st == CSA_OK && !mark(1, stream) ? CSA_ERR_CUDA : st;
+}
+
+// ---------------------------------------------------------------------------
+// Attention over a 4-bit cache.
+namespace {
+
+using CattnFn = void (*)(const csa::cattn::AttnParams);
+
+struct CattnPlan {
+    int nt;                 // n-tiles of 8 rows
+    int tiles, rows, splits;
+    long long works;
+    size_t workspace;
+    CattnFn fn;
+    int smem;
+};
+
+template <int kDk, int kDv>
+void cattn_pick(CattnPlan *pl)
+{
+    if (pl->nt == 1) {
+        pl->fn = csa::cattn::cache_attn_kernel<kDk, kDv, 1>;
+        pl->smem = csa::cattn::Shape<kDk, kDv, 1>::kSmem;
+    } else {
+        pl->fn = csa::cattn::cache_attn_kernel<kDk, kDv, 2>;
+        pl->smem = csa::cattn::Shape<kDk, kDv, 2>::kSmem;
+    }
+}
+
+template <int kDk>
+bool cattn_pick_dv(int dv, CattnPlan *pl)
+{
+    switch (dv) {
+    case 64: cattn_pick<kDk, 64>(pl); return true;
+    case 128: cattn_pick<kDk, 128>(pl); return true;
+    case 192: cattn_pick<kDk, 192>(pl); return true;
+    case 256: cattn_pick<kDk, 256>(pl); return true;
+    }
+    return false;
+}
+
+csa_status_t validate_cattn(const csa_cache_attn_args_t *a)
+{
+    if (!a || a->B < 0 || a->S < 0 || a->HA <= 0 || !std::isfinite(a->scale) || (a->idx && a->topk <= 0))
+        return CSA_ERR_INVALID_ARG;
+    csa_status_t st = validate_cache(a->cache_k);
+    if (st == CSA_OK)
+        st = validate_cache(a->cache_v);
+    if (st != CSA_OK)
+        return st;
+    if (!same_pages(a->cache_k, a->cache_v) || a->HA % a->cache_k.H != 0)
+        return CSA_ERR_INVALID_ARG;
+    const int dk = a->cache_k.D, dv = a->cache_v.D;
+    if (a->cache_k.dtype != CSA_CACHE_E2M1 || dk % 64 != 0 || dk > 256 || dv % 64 != 0 || dv > 256 ||
+        a->HA / a->cache_k.H > 128)
+        return CSA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(a->B) * a->S == 0)
+        return CSA_OK;
+    st = validate_pages(a->kv_len, a->page_table, a->max_pages, a->table_stride, a->cache_k.page_size);
+    if (st != CSA_OK)
+        return st;
+    if (!a->q || !a->out || !aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->idx, 4) ||
+        !aligned(a->lse, 4))
+        return CSA_ERR_INVALID_ARG;
+    if (static_cast<long long>(a->S) * a->HA >= kIntLimit || (a->idx && a->topk >= kIntLimit) ||
+        static_cast<long long>(a->B) * a->S * a->HA >= kIntLimit)
+        return CSA_ERR_UNSUPPORTED;
+    return CSA_OK;
+}
+
+csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
+{
+    const int sms = device_sms();
+    if (sms <= 0)
+        return CSA_ERR_CUDA;
+    const int H = a->cache_k.H, G = a->HA / H;
+    pl->rows = a->idx ? G : a->S * G;
+    pl->nt = pl->rows <= 8 ? 1 : 2;
+    pl->tiles = (pl->rows + 8 * pl->nt - 1) / (8 * pl->nt);
+    pl->works = static_cast<long long>(a->B) * (a->idx ? a->S : 1) * H * pl->tiles;
+    bool ok = false;
+    switch (a->cache_k.D) {
+    case 64: ok = cattn_pick_dv<64>(a->cache_v.D, pl); break;
+    case 128: ok = cattn_pick_dv<128>(a->cache_v.D, pl); break;
+    case 192: ok = cattn_pick_dv<192>(a->cache_v.D, pl); break;
+    case 256: ok = cattn_pick_dv<256>(a->cache_v.D, pl); break;
+    }
+    if (!ok)
+        return CSA_ERR_UNSUPPORTED;
+    // the keys are shared out until the GPU is full twice over, but a share is
+    // at least one block of 32 keys a warp
+    const long long most = a->idx ? a->topk : static_cast<long long>(a->max_pages) * a->cache_k.page_size;
+    const long long per = csa::cattn::kBlock * csa::cattn::kWarps;
+    long long splits = (6ll * sms + pl->works - 1) / pl->works;
+    if (splits > (most + per - 1) / per)
+        splits = (most + per - 1) / per;
+    pl->splits = static_cast<int>(splits < 1 ? 1 : splits > 256 ? 256 : splits);
+    if (pl->works * pl->splits >= kIntLimit)
+        return CSA_ERR_UNSUPPORTED;
+    pl->workspace = pl->splits > 1 ? static_cast<size_t>(pl->works) * pl->splits * 8 * pl->nt *
+                                         (a->cache_v.D + 2) * sizeof(float)
+                                   : 0;
+    return CSA_OK;
+}
+
+} // namespace
+
+extern "C" size_t csa_cache_attention_workspace_size(const csa_cache_attn_args_t *args)
+{
+    CattnPlan pl;
+    if (validate_cattn(args) != CSA_OK || static_cast<long long>(args->B) * args->S == 0 ||
+        plan_cattn(args, &pl) != CSA_OK)
+        return 0;
+    return pl.workspace;
+}
+
+extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, void *workspace,
+                                            size_t workspace_bytes, cudaStream_t stream)
+{
+    NvtxRange range("csa_cache_attention");
+    const csa_cache_attn_args_t *a = args;
+    csa_status_t st = validate_cattn(a);
+    if (st != CSA_OK)
+        return st;
+    if (static_cast<long long>(a->B) * a->S == 0)
+        return CSA_OK;
+    CattnPlan pl;
+    st = plan_cattn(a, &pl);
+    if (st != CSA_OK)
+        return st;
+    void *ws = workspace;
+    if (ws) {
+        if (workspace_bytes < pl.workspace)
+            return CSA_ERR_WORKSPACE;
+        if (!aligned(ws, 256))
+            return CSA_ERR_INVALID_ARG;
+    } else if (pl.workspace && cudaMallocAsync(&ws, pl.workspace, stream) != cudaSuccess) {
+        return CSA_ERR_CUDA;
+    }
+    csa::cattn::AttnParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q = static_cast<const __nv_bfloat16 *>(a->q);
+    p.ck = cache_view(a->cache_k);
+    p.cv = cache_view(a->cache_v);
+    p.pm = page_map(a->cache_k, a->page_table, a->max_pages, a->table_stride);
+    p.kv_len = a->kv_len;
+    p.idx = a->idx;
+    p.topk = a->topk;
+    p.B = a->B;
+    p.S = a->S;
+    p.HA = a->HA;
+    p.H = a->cache_k.H;
+    p.G = p.HA / p.H;
+    p.causal = a->causal != 0;
+    p.sl2 = a->scale * a->cache_k.tensor_scale * 1.4426950408889634f;
+    p.v_scale = a->cache_v.tensor_scale;
+    p.out = static_cast<__nv_bfloat16 *>(a->out);
+    p.lse = a->lse;
+    p.splits = pl.splits;
+    p.tiles = pl.tiles;
+    p.rows = pl.rows;
+    p.capacity = a->max_pages * a->cache_k.page_size;
+    p.part = static_cast<float *>(ws);
+    if (cudaFuncSetAttribute(pl.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem) != cudaSuccess ||
+        !mark(0, stream))
+        st = CSA_ERR_CUDA;
+    if (st == CSA_OK) {
+        pl.fn<<<static_cast<unsigned>(pl.works * pl.splits), csa::cattn::kThreads, pl.smem, stream>>>(p);
+        st = launched();
+    }
+    if (st == CSA_OK && !mark(1, stream))
+        st = CSA_ERR_CUDA;
+    if (st == CSA_OK && pl.splits > 1) {
+        const long long rows = static_cast<long long>(a->B) * a->S * a->HA;
+        csa::cattn::cache_attn_join_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(
+            p, a->cache_v.D, 8 * pl.nt, rows);
+        st = launched();
+        if (st == CSA_OK && !mark(2, stream))
+            st = CSA_ERR_CUDA;
+    }
+    if (!workspace && ws && cudaFreeAsync(ws, stream) != cudaSuccess && st == CSA_OK)
+        st = CSA_ERR_CUDA;
+    return st;
+}

@@ -1041,6 +1041,8 @@ extern "C" csa_status_t csa_indexer_topk_noalloc(const csa_args_t *args, cudaStr
     return launch(args, plan, scratch, stream);
 }
 
+#include "cache_host.cuh"
+
 #ifdef CSA_PROFILE
 // Profiling build only: per-CTA role counters of the last launches.
 extern "C" int csa_profile_read(unsigned long long *out, int n)
