@@ -5,6 +5,7 @@
 
 #include "csa_cache.h"
 #include "cache_attn_kernel.cuh"
+#include "cache_attn_wide_kernel.cuh"
 #include "cache_rows_kernel.cuh"
 #include "rotary_kernel.cuh"
 
@@ -402,25 +403,31 @@ extern "C" csa_status_t csa_cache_read(const csa_cache_read_args_t *args, cudaSt
 namespace {
 
 using CattnFn = void (*)(const csa::cattn::AttnParams);
+using CattnWideFn = void (*)(const csa::cattn::WideParams);
 
 struct CattnPlan {
-    int nt;                 // n-tiles of 8 rows
-    int tiles, rows, splits;
+    bool wide;
+    int tile_rows, tiles, rows, splits;
     long long works;
     size_t workspace;
     CattnFn fn;
+    CattnWideFn wide_fn;
     int smem;
 };
 
 template <int kDk, int kDv>
 void cattn_pick(CattnPlan *pl)
 {
-    if (pl->nt == 1) {
-        pl->fn = csa::cattn::cache_attn_kernel<kDk, kDv, 1>;
-        pl->smem = csa::cattn::Shape<kDk, kDv, 1>::kSmem;
+    using namespace csa::cattn;
+    if (pl->wide) {
+        pl->wide_fn = pl->tile_rows == kWideRows ? cache_attn_wide_kernel<kDk, kDv, false>
+                                                 : cache_attn_wide_kernel<kDk, kDv, true>;
+    } else if (pl->tile_rows == 8) {
+        pl->fn = cache_attn_kernel<kDk, kDv, 1>;
+        pl->smem = Shape<kDk, kDv, 1>::kSmem;
     } else {
-        pl->fn = csa::cattn::cache_attn_kernel<kDk, kDv, 2>;
-        pl->smem = csa::cattn::Shape<kDk, kDv, 2>::kSmem;
+        pl->fn = cache_attn_kernel<kDk, kDv, 2>;
+        pl->smem = Shape<kDk, kDv, 2>::kSmem;
     }
 }
 
@@ -472,8 +479,9 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
         return CSA_ERR_CUDA;
     const int H = a->cache_k.H, G = a->HA / H;
     pl->rows = a->idx ? G : a->S * G;
-    pl->nt = pl->rows <= 8 ? 1 : 2;
-    pl->tiles = (pl->rows + 8 * pl->nt - 1) / (8 * pl->nt);
+    pl->wide = pl->rows > 16;
+    pl->tile_rows = pl->rows <= 8 ? 8 : pl->rows <= 16 ? 16 : pl->rows <= 64 ? 64 : csa::cattn::kWideRows;
+    pl->tiles = (pl->rows + pl->tile_rows - 1) / pl->tile_rows;
     pl->works = static_cast<long long>(a->B) * (a->idx ? a->S : 1) * H * pl->tiles;
     bool ok = false;
     switch (a->cache_k.D) {
@@ -484,20 +492,76 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
     }
     if (!ok)
         return CSA_ERR_UNSUPPORTED;
-    // the keys are shared out until the GPU is full twice over, but a share is
-    // at least one block of 32 keys a warp
     const long long most = a->idx ? a->topk : static_cast<long long>(a->max_pages) * a->cache_k.page_size;
-    const long long per = csa::cattn::kBlock * csa::cattn::kWarps;
-    long long splits = (6ll * sms + pl->works - 1) / pl->works;
-    if (splits > (most + per - 1) / per)
-        splits = (most + per - 1) / per;
+    long long splits = 1;
+    if (pl->wide) {
+        // the share count that ends first: rounds of the persistent grid x tiles
+        // of a share, an item costing about three tiles of its own
+        const long long tiles = (most + csa::cattn::kWideKeys - 1) / csa::cattn::kWideKeys;
+        long long best = -1;
+        for (long long s = 1; s <= tiles && s <= 256; ++s) {
+            const long long cost = (pl->works * s + sms - 1) / sms * ((tiles + s - 1) / s + 3);
+            if (best < 0 || cost < best) {
+                best = cost;
+                splits = s;
+            }
+        }
+    } else {
+        // the keys are shared out until the GPU is full twice over, but a share is
+        // at least one block of 32 keys a warp
+        const long long per = csa::cattn::kBlock * csa::cattn::kWarps;
+        splits = (6ll * sms + pl->works - 1) / pl->works;
+        if (splits > (most + per - 1) / per)
+            splits = (most + per - 1) / per;
+    }
     pl->splits = static_cast<int>(splits < 1 ? 1 : splits > 256 ? 256 : splits);
     if (pl->works * pl->splits >= kIntLimit)
         return CSA_ERR_UNSUPPORTED;
-    pl->workspace = pl->splits > 1 ? static_cast<size_t>(pl->works) * pl->splits * 8 * pl->nt *
+    pl->workspace = pl->splits > 1 ? static_cast<size_t>(pl->works) * pl->splits * pl->tile_rows *
                                          (a->cache_v.D + 2) * sizeof(float)
                                    : 0;
     return CSA_OK;
+}
+
+// The tiles' launch: the persistent tcgen05 kernel.
+csa_status_t launch_wide(const csa_cache_attn_args_t *a, const CattnPlan &pl, const csa::cattn::AttnParams &p,
+                         cudaStream_t stream)
+{
+    using namespace csa::cattn;
+    WideParams w;
+    std::memset(&w, 0, sizeof w);
+    w.a = p;
+    w.items = static_cast<int>(pl.works * pl.splits);
+    w.k_bytes = kWideKeys * a->cache_k.D * 2;
+    w.v_bytes = kWideKeys * a->cache_v.D * 2;
+    const int x_bytes = pl.tile_rows == kWideRows ? 0 : 4 * 32 * 32 * 4;
+    const int fixed = x_bytes + static_cast<int>(sizeof(WideBarriers)) + 1024;
+    // as many stages as fit, the keys' ring first
+    static const int kChoices[5][2] = {{3, 3}, {3, 2}, {2, 2}, {2, 1}, {1, 1}};
+    for (const auto &c : kChoices)
+        if (fixed + c[0] * w.k_bytes + c[1] * w.v_bytes <= kSmemLimit) {
+            w.k_stages = c[0];
+            w.v_stages = c[1];
+            break;
+        }
+    if (w.k_stages == 0)
+        return CSA_ERR_UNSUPPORTED;
+    w.off_v = w.k_stages * w.k_bytes;
+    w.off_x = w.off_v + w.v_stages * w.v_bytes;
+    w.off_bar = w.off_x + x_bytes;
+    // more than half of the SM: one CTA a SM, so its TMEM allocation never waits
+    int smem = w.off_bar + static_cast<int>(sizeof(WideBarriers)) + 1024;
+    smem = smem < kSmemLimit / 2 + 1024 ? kSmemLimit / 2 + 1024 : smem;
+    // TMEM columns: S slots, O, Q (two elements a column)
+    w.slots = 2 * kWideKeys + a->cache_v.D + a->cache_k.D / 2 <= 512 ? 2 : 1;
+    w.col_o = w.slots * kWideKeys;
+    w.col_q = w.col_o + a->cache_v.D;
+    w.wait_limit = static_cast<long long>(g_wait_limit);
+    const int sms = device_sms();
+    if (sms <= 0 || cudaFuncSetAttribute(pl.wide_fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return CSA_ERR_CUDA;
+    pl.wide_fn<<<w.items < sms ? w.items : sms, kWideThreads, smem, stream>>>(w);
+    return launched();
 }
 
 } // namespace
@@ -558,10 +622,13 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     p.rows = pl.rows;
     p.capacity = a->max_pages * a->cache_k.page_size;
     p.part = static_cast<float *>(ws);
-    if (cudaFuncSetAttribute(pl.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem) != cudaSuccess ||
-        !mark(0, stream))
+    if (!mark(0, stream)) {
         st = CSA_ERR_CUDA;
-    if (st == CSA_OK) {
+    } else if (pl.wide) {
+        st = launch_wide(a, pl, p, stream);
+    } else if (cudaFuncSetAttribute(pl.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem) != cudaSuccess) {
+        st = CSA_ERR_CUDA;
+    } else {
         pl.fn<<<static_cast<unsigned>(pl.works * pl.splits), csa::cattn::kThreads, pl.smem, stream>>>(p);
         st = launched();
     }
@@ -570,7 +637,7 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     if (st == CSA_OK && pl.splits > 1) {
         const long long rows = static_cast<long long>(a->B) * a->S * a->HA;
         csa::cattn::cache_attn_join_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(
-            p, a->cache_v.D, 8 * pl.nt, rows);
+            p, a->cache_v.D, pl.tile_rows, rows);
         st = launched();
         if (st == CSA_OK && !mark(2, stream))
             st = CSA_ERR_CUDA;
