@@ -71,6 +71,7 @@ struct AttnParams {
     int rows;                               // query rows of a group: S * G, or G with idx
     int capacity;                           // positions the page table reaches
     float *part;                            // [work][split][rows of a tile][Dv + 2]
+    FastDiv div_splits, div_tiles, div_H, div_S, div_G;
 };
 
 // The group of query rows that a work item belongs to.
@@ -82,16 +83,16 @@ struct Group {
 __device__ __forceinline__ Group group_of(const AttnParams &p, int w, int tile_rows)
 {
     Group g;
-    g.r0 = (w % p.tiles) * tile_rows;
-    w /= p.tiles;
-    g.h = w % p.H;
-    w /= p.H;
+    int q = static_cast<int>(p.div_tiles.div(w));
+    g.r0 = (w - q * p.tiles) * tile_rows;
+    w = q;
+    q = static_cast<int>(p.div_H.div(w));
+    g.h = w - q * p.H;
+    g.b = q;
+    g.i0 = 0;
     if (p.idx) {
-        g.i0 = w % p.S;
-        g.b = w / p.S;
-    } else {
-        g.i0 = 0;
-        g.b = w;
+        g.b = static_cast<int>(p.div_S.div(q));
+        g.i0 = q - g.b * p.S;
     }
     return g;
 }
@@ -99,7 +100,7 @@ __device__ __forceinline__ Group group_of(const AttnParams &p, int w, int tile_r
 // Query and head of row r of a group.
 __device__ __forceinline__ void row_of(const AttnParams &p, const Group &g, int r, int &i, int &head)
 {
-    const int k = r / p.G;
+    const int k = static_cast<int>(p.div_G.div(r));
     i = g.i0 + k;
     head = g.h * p.G + r - k * p.G;
 }
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 && kDk + kDv <= 256 ? 3 : 2
     extern __shared__ float smem[];                      // [warp][row][Dv + 2]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int work = blockIdx.x / p.splits, split = blockIdx.x - work * p.splits;
+    const int work = static_cast<int>(p.div_splits.div(blockIdx.x)), split = blockIdx.x - work * p.splits;
     const Group gr = group_of(p, work, RT);
     const int len = __ldg(p.kv_len + gr.b);
     const int32_t *table = p.pm.table + gr.b * p.pm.table_stride;
@@ -243,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 && kDk + kDv <= 256 ? 3 : 2
 
     // the tile's rows: what the last and the first of them see
     const int r_last = min(gr.r0 + RT, p.rows) - 1;
-    const int see_hi = len > 0 ? seen(p, len, gr.i0 + r_last / p.G) : 0;
-    const int see_lo = len > 0 ? seen(p, len, gr.i0 + gr.r0 / p.G) : 0;
+    const int see_hi = len > 0 ? seen(p, len, gr.i0 + static_cast<int>(p.div_G.div(r_last))) : 0;
+    const int see_lo = len > 0 ? seen(p, len, gr.i0 + static_cast<int>(p.div_G.div(gr.r0))) : 0;
     const int slots = p.idx ? (see_hi > 0 ? p.topk : 0) : min(max(see_hi, 0), p.capacity);
     const int blocks = (slots + kBlock - 1) / kBlock;
     const int b_lo = static_cast<int>(static_cast<long long>(blocks) * split / p.splits);

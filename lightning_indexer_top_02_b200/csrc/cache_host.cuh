@@ -407,6 +407,7 @@ using CattnWideFn = void (*)(const csa::cattn::WideParams);
 
 struct CattnPlan {
     bool wide;
+    int keys, raw;          // of the wide kernel: keys of a tile, staging bytes
     int tile_rows, tiles, rows, splits;
     long long works;
     size_t workspace;
@@ -420,6 +421,8 @@ void cattn_pick(CattnPlan *pl)
 {
     using namespace csa::cattn;
     if (pl->wide) {
+        pl->keys = WideShape<kDk, kDv>::kKeys;
+        pl->raw = 2 * kGatherWarps * WideShape<kDk, kDv>::kRaw;
         pl->wide_fn = pl->tile_rows == kWideRows ? cache_attn_wide_kernel<kDk, kDv, false>
                                                  : cache_attn_wide_kernel<kDk, kDv, true>;
     } else if (pl->tile_rows == 8) {
@@ -497,7 +500,7 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
     if (pl->wide) {
         // the share count that ends first: rounds of the persistent grid x tiles
         // of a share, an item costing about three tiles of its own
-        const long long tiles = (most + csa::cattn::kWideKeys - 1) / csa::cattn::kWideKeys;
+        const long long tiles = (most + pl->keys - 1) / pl->keys;
         long long best = -1;
         for (long long s = 1; s <= tiles && s <= 256; ++s) {
             const long long cost = (pl->works * s + sms - 1) / sms * ((tiles + s - 1) / s + 3);
@@ -532,12 +535,13 @@ csa_status_t launch_wide(const csa_cache_attn_args_t *a, const CattnPlan &pl, co
     std::memset(&w, 0, sizeof w);
     w.a = p;
     w.items = static_cast<int>(pl.works * pl.splits);
-    w.k_bytes = kWideKeys * a->cache_k.D * 2;
-    w.v_bytes = kWideKeys * a->cache_v.D * 2;
-    const int x_bytes = pl.tile_rows == kWideRows ? 0 : 4 * 32 * 32 * 4;
-    const int fixed = x_bytes + static_cast<int>(sizeof(WideBarriers)) + 1024;
-    // as many stages as fit, the keys' ring first
-    static const int kChoices[5][2] = {{3, 3}, {3, 2}, {2, 2}, {2, 1}, {1, 1}};
+    w.k_bytes = pl.keys * a->cache_k.D * 2;
+    w.v_bytes = pl.keys * a->cache_v.D * 2;
+    const int q_bytes = kWideRows * a->cache_k.D * 2;
+    const int x_bytes = pl.tile_rows == kWideRows ? 0 : 4 * kXCols * 32 * 4;
+    const int fixed = q_bytes + pl.raw + x_bytes + static_cast<int>(sizeof(WideBarriers)) + 1024;
+    // as many stages as fit
+    static const int kChoices[4][2] = {{2, 2}, {2, 1}, {1, 2}, {1, 1}};
     for (const auto &c : kChoices)
         if (fixed + c[0] * w.k_bytes + c[1] * w.v_bytes <= kSmemLimit) {
             w.k_stages = c[0];
@@ -546,20 +550,25 @@ csa_status_t launch_wide(const csa_cache_attn_args_t *a, const CattnPlan &pl, co
         }
     if (w.k_stages == 0)
         return CSA_ERR_UNSUPPORTED;
-    w.off_v = w.k_stages * w.k_bytes;
-    w.off_x = w.off_v + w.v_stages * w.v_bytes;
+    w.off_k = q_bytes;
+    w.off_v = w.off_k + w.k_stages * w.k_bytes;
+    w.off_raw = w.off_v + w.v_stages * w.v_bytes;
+    w.off_x = w.off_raw + pl.raw;
     w.off_bar = w.off_x + x_bytes;
     // more than half of the SM: one CTA a SM, so its TMEM allocation never waits
     int smem = w.off_bar + static_cast<int>(sizeof(WideBarriers)) + 1024;
     smem = smem < kSmemLimit / 2 + 1024 ? kSmemLimit / 2 + 1024 : smem;
-    // TMEM columns: S slots, O, Q (two elements a column)
-    w.slots = 2 * kWideKeys + a->cache_v.D + a->cache_k.D / 2 <= 512 ? 2 : 1;
-    w.col_o = w.slots * kWideKeys;
-    w.col_q = w.col_o + a->cache_v.D;
     w.wait_limit = static_cast<long long>(g_wait_limit);
     const int sms = device_sms();
     if (sms <= 0 || cudaFuncSetAttribute(pl.wide_fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return CSA_ERR_CUDA;
+    // the warpgroups trade registers (setmaxnreg): only valid for a build with
+    // exactly the launch count that the split assumes
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, pl.wide_fn) != cudaSuccess)
+        return CSA_ERR_CUDA;
+    if (fa.numRegs != kWideLaunchRegs)
+        return CSA_ERR_UNSUPPORTED;
     pl.wide_fn<<<w.items < sms ? w.items : sms, kWideThreads, smem, stream>>>(w);
     return launched();
 }
@@ -621,6 +630,11 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     p.tiles = pl.tiles;
     p.rows = pl.rows;
     p.capacity = a->max_pages * a->cache_k.page_size;
+    p.div_splits = FastDiv::of(p.splits);
+    p.div_tiles = FastDiv::of(p.tiles);
+    p.div_H = FastDiv::of(p.H);
+    p.div_S = FastDiv::of(p.S);
+    p.div_G = FastDiv::of(p.G);
     p.part = static_cast<float *>(ws);
     if (!mark(0, stream)) {
         st = CSA_ERR_CUDA;
