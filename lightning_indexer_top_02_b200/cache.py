@@ -133,8 +133,10 @@ def make_cache(dtype: str, num_pages: int, page_size: int, H: int, D: int, *, de
                  torch.zeros(shape + (D // 16,), dtype=torch.uint8, device=device), tensor_scale)
 
 
-def _dense_but_pages(name, t):
-    """The stride in bytes from page to page of a tensor that is dense within a page."""
+def _page_stride(name, t):
+    """Bytes from page to page of a tensor that is dense within a page (0: dense altogether)."""
+    if t.is_contiguous():
+        return 0
     n = 1
     for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if size != 1 and stride != n:
@@ -143,50 +145,53 @@ def _dense_but_pages(name, t):
     return (t.stride(0) if t.shape[0] > 1 else n) * t.element_size()
 
 
-def _cache_struct(name: str, c: Cache, device) -> CsaCache:
+def _cache_struct(name: str, c: Cache) -> CsaCache:
     import torch
 
-    if c.dtype not in CACHE_DTYPES:
+    kind = CACHE_DTYPES.get(c.dtype)
+    if kind is None:
         raise ValueError(f"unknown cache type {c.dtype!r}")
     data, scale = c.data, c.scale
-    want = (torch.bfloat16,) if c.dtype == "bf16" else (torch.uint8, torch.float8_e4m3fn) if c.dtype == "e4m3" \
-        else (torch.uint8,)
-    if data.dtype not in want or data.dim() != 4:
-        raise TypeError(f"{name}.data must be a 4-dimensional {want[0]} tensor")
-    s = CsaCache()
-    s.dtype = CACHE_DTYPES[c.dtype]
-    s.num_pages, s.H, s.page_size = data.shape[:3]
-    s.D = c.D
-    _on(device, **{name + ".data": data})
-    s.data, s.page_stride = data.data_ptr(), _dense_but_pages(name + ".data", data)
-    if c.dtype != "bf16":
-        kinds = (torch.float32,) if c.dtype == "e4m3" else (torch.uint8, torch.float8_e4m3fn)
-        tail = () if c.dtype == "e4m3" else (s.D // 16,)
-        if scale is None or scale.dtype not in kinds or tuple(scale.shape) != tuple(data.shape[:3]) + tail:
-            raise TypeError(f"{name}.scale must be {kinds[0]} {tuple(data.shape[:3]) + tail}")
-        _on(device, **{name + ".scale": scale})
-        s.scale, s.scale_page_stride = scale.data_ptr(), _dense_but_pages(name + ".scale", scale)
-    s.tensor_scale = float(c.tensor_scale)
-    return s
+    shape = data.shape
+    want = torch.bfloat16 if kind == CSA_CACHE_BF16 else torch.uint8
+    if len(shape) != 4 or (data.dtype != want and not (kind == CSA_CACHE_E4M3 and data.dtype == torch.float8_e4m3fn)):
+        raise TypeError(f"{name}.data must be a 4-dimensional {want} tensor")
+    D = shape[3] * 2 if kind == CSA_CACHE_E2M1 else shape[3]
+    if kind == CSA_CACHE_BF16:
+        return CsaCache(data.data_ptr(), None, kind, shape[1], D, shape[0], shape[2],
+                        _page_stride(name + ".data", data), 0, c.tensor_scale)
+    tail = shape[:3] if kind == CSA_CACHE_E4M3 else shape[:3] + (D // 16,)
+    want = torch.float32 if kind == CSA_CACHE_E4M3 else torch.uint8
+    if scale is None or scale.shape != tail or \
+            (scale.dtype != want and not (kind == CSA_CACHE_E2M1 and scale.dtype == torch.float8_e4m3fn)):
+        raise TypeError(f"{name}.scale must be {want} {tuple(tail)}")
+    return CsaCache(data.data_ptr(), scale.data_ptr(), kind, shape[1], D, shape[0], shape[2],
+                    _page_stride(name + ".data", data), _page_stride(name + ".scale", scale), c.tensor_scale)
 
 
-def _on(device, **tensors):
+def _on(dev, **tensors):
+    """Every tensor (a cache: its two) on one CUDA device, and none that would need a gradient."""
     import torch
 
+    grad = torch.is_grad_enabled()
     for name, t in tensors.items():
         if t is None:
             continue
-        if not t.is_cuda or t.device != device:
-            raise ValueError(f"{name} must be on {device}")
-        if t.requires_grad and torch.is_grad_enabled():
+        if isinstance(t, Cache):
+            _on(dev, **{name + ".data": t.data, name + ".scale": t.scale})
+            continue
+        if t.get_device() != dev or dev < 0:
+            raise ValueError(f"{name} must be on " + (f"CUDA device {dev}" if dev >= 0 else "a CUDA device"))
+        if grad and t.requires_grad:
             raise ValueError(f"{name} needs a gradient, which this call does not record")
 
 
 def _int32(name, t, shape):
     import torch
 
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
+    return t.data_ptr()
 
 
 def _freq(inv_freq):
@@ -194,17 +199,19 @@ def _freq(inv_freq):
 
     if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a contiguous float32 vector")
+    return inv_freq.data_ptr()
 
 
 def _table(page_table, kv_len):
+    """(kv_len, page_table, max_pages, table_stride) for the argument structs, after B."""
     import torch
 
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or \
             (page_table.shape[1] > 1 and page_table.stride(1) != 1):
         raise TypeError("page_table must be int32 [B, max_pages] with dense rows")
-    _int32("kv_len", kv_len, (page_table.shape[0],))
     B, n = page_table.shape
-    return B, n, page_table.stride(0) if B > 1 else n
+    lens = _int32("kv_len", kv_len, (B,))
+    return B, (lens, page_table.data_ptr(), n, page_table.stride(0) if B > 1 else n)
 
 
 @contextlib.contextmanager
@@ -216,16 +223,25 @@ def _elsewhere(device, stream):
 
 
 def _launch(t, stream):
-    """The call's stream, and a context in which the tensor's device is current
-    and allocations belong to that stream (memory handed out on another one
-    could still be in use there)."""
+    """The call's stream handle, and a context in which the tensor's device is
+    current and allocations belong to that stream (memory handed out on another one
+    could still be in use there); None where both already are."""
     import torch
 
-    here = torch.cuda.current_stream(t.device)
+    dev = t.get_device()
+    here = torch.cuda.current_stream(dev) if stream is not None or dev != torch.cuda.current_device() else None
+    if here is None:
+        return torch._C._cuda_getCurrentRawStream(dev), None
     if stream is None:
         stream = here
-    same = stream == here and torch.cuda.current_device() == t.device.index
-    return stream, contextlib.nullcontext() if same else _elsewhere(t.device, stream)
+    return stream.cuda_stream, _elsewhere(dev, stream)
+
+
+def _within(ctx, fn, *args, **kw):
+    if ctx is None:
+        return fn(*args, **kw)
+    with ctx:
+        return fn(*args, **kw)
 
 
 def _check(status, what):
@@ -257,36 +273,37 @@ def rotary(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = F
     place).  ``inverse`` rotates back: the gradient."""
     import torch
 
-    kinds = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    if x.dtype not in kinds or x.dim() < 2:
+    kind = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(x.dtype)
+    shape = x.shape
+    if kind is None or len(shape) < 2:
         raise TypeError("x must be a bfloat16, float16 or float32 tensor [..., H, D]")
-    _int32("positions", positions, x.shape[:-2])
-    _freq(inv_freq)
-    s, ctx = _launch(x, stream)
-    if out is None:
-        with ctx:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype:
+    dev = x.get_device()
+    pos = _int32("positions", positions, shape[:-2])
+    freq = _freq(inv_freq)
+    xs = _token_strides("x", x)
+    if out is not None and (out.shape != shape or out.dtype != x.dtype):
         raise TypeError("out must have the shape and type of x")
-    _on(x.device, x=x, positions=positions, inv_freq=inv_freq, out=out)
-    a = CsaRotaryArgs()
-    a.x, a.out, a.dtype = x.data_ptr(), out.data_ptr(), kinds[x.dtype]
-    a.H, a.D = x.shape[-2:]
-    a.N = positions.numel()
-    a.x_token_stride, a.x_head_stride = _token_strides("x", x)
-    a.out_token_stride, a.out_head_stride = _token_strides("out", out)
-    a.positions, a.inv_freq = positions.data_ptr(), inv_freq.data_ptr()
-    a.rot_dim, a.rot_offset = 2 * inv_freq.numel(), int(rot_offset)
-    a.interleaved, a.inverse, a.scale = int(bool(interleaved)), int(bool(inverse)), float(scale)
-    if x.numel() == 0:
+    _on(dev, x=x, positions=positions, inv_freq=inv_freq, out=out)
+    s, ctx = _launch(x, stream)
+
+    def call(out):
+        if out is None:
+            out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        if x.numel():
+            os = xs if out is x else _token_strides("out", out)
+            _check(csa_rotary(CsaRotaryArgs(x.data_ptr(), out.data_ptr(), kind, positions.numel(), shape[-2], shape[-1],
+                                            *xs, *os, pos, freq, 2 * inv_freq.numel(), rot_offset,
+                                            bool(interleaved), bool(inverse), scale), s), "csa_rotary")
         return out
-    with _launch(x, stream)[1]:
-        _check(csa_rotary(a, ctypes.c_void_p(s.cuda_stream)), "csa_rotary")
-    return out
+
+    return _within(ctx, call, out)
 
 
 def _token_strides(name, x):
     """(token, head) strides of [..., H, D] whose leading dimensions step evenly."""
+    if x.is_contiguous():
+        D = x.shape[-1]
+        return x.shape[-2] * D, D
     if x.shape[-1] > 1 and x.stride(-1) != 1:
         raise ValueError(f"{name}: a head's elements must be adjacent")
     step = None
@@ -312,64 +329,55 @@ def cache_append(k, cache_k: Cache, page_table, kv_len, *, v=None, cache_v: Opti
     already (0: an unused place); ``page_table`` int32 [B, max_pages]."""
     import torch
 
-    B, n, stride = _table(page_table, kv_len)
+    dev = k.get_device()
+    B, pages = _table(page_table, kv_len)
     if (v is None) != (cache_v is None):
         raise ValueError("v and cache_v go together")
-    lead = k.shape[:-2]
-    if k.dim() != (4 if cu_tokens is None else 3) or (cu_tokens is None and k.shape[0] != B):
+    shape = k.shape
+    lead = shape[:-2]
+    if len(shape) != (4 if cu_tokens is None else 3) or (cu_tokens is None and shape[0] != B):
         raise ValueError("k must be [B, S, H, Dk], or [N, H, Dk] with cu_tokens")
-    a = CsaAppendArgs()
-    for name, x, c in (("k", k, cache_k), ("v", v, cache_v)):
-        if x is None:
-            continue
-        if x.dtype != torch.bfloat16 or x.shape[:-2] != lead or x.shape[-2] != c.data.shape[1] or x.shape[-1] != c.D:
+
+    def rows(name, x, c):
+        st = _cache_struct("cache_" + name, c)
+        if x.dtype != torch.bfloat16 or x.shape[:-2] != lead or x.shape[-2] != st.H or x.shape[-1] != st.D:
             raise TypeError(f"{name} must be bfloat16 with the tokens of k and the heads and D of cache_{name}")
-        token, head = _token_strides(name, x)
-        setattr(a, name, x.data_ptr())
-        setattr(a, name + "_token_stride", token)
-        setattr(a, name + "_head_stride", head)
-        setattr(a, "cache_" + name, _cache_struct("cache_" + name, c, k.device))
-    a.N = k.shape[0] if cu_tokens is not None else k.shape[0] * k.shape[1]
-    a.B, a.S = B, 0 if cu_tokens is not None else k.shape[1]
-    if cu_tokens is not None:
-        _int32("cu_tokens", cu_tokens, (B + 1,))
-        a.cu_tokens = cu_tokens.data_ptr()
-    if positions is not None:
-        _int32("positions", positions, lead)
-        a.positions = positions.data_ptr()
-    if inv_freq is not None:
-        _freq(inv_freq)
-        a.inv_freq, a.rot_dim, a.rot_offset = inv_freq.data_ptr(), 2 * inv_freq.numel(), int(rot_offset)
-        a.interleaved, a.rope_scale = int(bool(interleaved)), float(rope_scale)
-    _on(k.device, k=k, v=v, page_table=page_table, kv_len=kv_len, cu_tokens=cu_tokens, positions=positions,
-        inv_freq=inv_freq)
-    a.kv_len, a.page_table, a.max_pages, a.table_stride = kv_len.data_ptr(), page_table.data_ptr(), n, stride
+        return x.data_ptr(), _token_strides(name, x), st
+
+    kp, ks, kc = rows("k", k, cache_k)
+    vp, vs, vc = rows("v", v, cache_v) if v is not None else (None, (0, 0), kc)
+    N, S = (shape[0], 0) if cu_tokens is not None else (shape[0] * shape[1], shape[1])
+    cu = _int32("cu_tokens", cu_tokens, (B + 1,)) if cu_tokens is not None else None
+    pos = _int32("positions", positions, lead) if positions is not None else None
+    freq, rot = (_freq(inv_freq), 2 * inv_freq.numel()) if inv_freq is not None else (None, 0)
+    _on(dev, k=k, cache_k=cache_k, v=v, cache_v=cache_v, page_table=page_table, kv_len=kv_len, cu_tokens=cu_tokens,
+        positions=positions, inv_freq=inv_freq)
+    a = CsaAppendArgs(kp, vp, *ks, *vs, N, B, S, cu, *pages, kc, vc, freq, pos, rot, rot_offset, bool(interleaved),
+                      rope_scale)
     s, ctx = _launch(k, stream)
-    with ctx:
-        _check(csa_cache_append(a, ctypes.c_void_p(s.cuda_stream)), "csa_cache_append")
+    _check(_within(ctx, csa_cache_append, a, s), "csa_cache_append")
 
 
 def cache_read(cache: Cache, page_table, kv_len, T: int, *, out=None, stream=None):
     """Positions 0 .. T-1 of every sequence as bf16 [B, T, H, D], zeros past ``kv_len``."""
     import torch
 
-    B, n, stride = _table(page_table, kv_len)
-    dev = cache.data.device
-    a = CsaCacheReadArgs()
-    a.cache = _cache_struct("cache", cache, dev)
-    shape = (B, int(T), a.cache.H, a.cache.D)
-    s, ctx = _launch(cache.data, stream)
-    if out is None:
-        with ctx:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    elif out.dtype != torch.bfloat16 or tuple(out.shape) != shape or not out.is_contiguous():
+    dev = cache.data.get_device()
+    B, pages = _table(page_table, kv_len)
+    c = _cache_struct("cache", cache)
+    shape = (B, int(T), c.H, c.D)
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous()):
         raise TypeError(f"out must be a contiguous bfloat16 tensor of shape {shape}")
-    _on(dev, page_table=page_table, kv_len=kv_len, out=out)
-    a.kv_len, a.page_table, a.max_pages, a.table_stride = kv_len.data_ptr(), page_table.data_ptr(), n, stride
-    a.B, a.T, a.out = B, int(T), out.data_ptr()
-    with _launch(cache.data, stream)[1]:
-        _check(csa_cache_read(a, ctypes.c_void_p(s.cuda_stream)), "csa_cache_read")
-    return out
+    _on(dev, cache=cache, page_table=page_table, kv_len=kv_len, out=out)
+    s, ctx = _launch(cache.data, stream)
+
+    def call(out):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=cache.data.device)
+        _check(csa_cache_read(CsaCacheReadArgs(c, *pages, B, shape[1], out.data_ptr()), s), "csa_cache_read")
+        return out
+
+    return _within(ctx, call, out)
 
 
 def cache_attention(q, cache_k: Cache, cache_v: Cache, page_table, kv_len, *, scale: float, idx=None,
@@ -380,37 +388,35 @@ def cache_attention(q, cache_k: Cache, cache_v: Cache, page_table, kv_len, *, sc
     ``workspace`` (uint8 CUDA tensor) is allocated if not given."""
     import torch
 
-    B, n, stride = _table(page_table, kv_len)
-    if q.dtype != torch.bfloat16 or q.dim() != 4 or q.shape[0] != B or not q.is_contiguous() \
-            or q.shape[-1] != cache_k.D:
+    dev = q.get_device()
+    B, pages = _table(page_table, kv_len)
+    kc, vc = _cache_struct("cache_k", cache_k), _cache_struct("cache_v", cache_v)
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or q.shape[0] != B or not q.is_contiguous() or q.shape[-1] != kc.D:
         raise TypeError("q must be a contiguous bfloat16 tensor [B, S, HA, Dk]")
-    S, HA = q.shape[1:3]
-    a = CsaCacheAttnArgs()
-    a.cache_k = _cache_struct("cache_k", cache_k, q.device)
-    a.cache_v = _cache_struct("cache_v", cache_v, q.device)
-    if idx is not None:
-        _int32("idx", idx, (B, S, idx.shape[-1]))
-        a.idx, a.topk = idx.data_ptr(), idx.shape[-1]
-    for name, t, dtype, shape in (("out", out, torch.bfloat16, (B, S, HA, a.cache_v.D)),
+    _, S, HA, _ = q.shape
+    ip, topk = (None, 0) if idx is None else (_int32("idx", idx, (B, S, idx.shape[-1])), idx.shape[-1])
+    for name, t, dtype, shape in (("out", out, torch.bfloat16, (B, S, HA, vc.D)),
                                   ("lse", lse, torch.float32, (B, S, HA))):
-        if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous()):
+        if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
             raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    _on(dev, q=q, cache_k=cache_k, cache_v=cache_v, page_table=page_table, kv_len=kv_len, idx=idx, out=out, lse=lse,
+        workspace=workspace)
     s, ctx = _launch(q, stream)
-    with ctx:
+
+    def call(out, lse, workspace):
         if out is None:
-            out = torch.empty((B, S, HA, a.cache_v.D), dtype=torch.bfloat16, device=q.device)
+            out = torch.empty((B, S, HA, vc.D), dtype=torch.bfloat16, device=q.device)
         if lse is None and return_lse:
             lse = torch.empty((B, S, HA), dtype=torch.float32, device=q.device)
-        _on(q.device, q=q, page_table=page_table, kv_len=kv_len, idx=idx, out=out, lse=lse, workspace=workspace)
-        a.q, a.out = q.data_ptr(), out.data_ptr()
-        a.lse = lse.data_ptr() if lse is not None else None
-        a.kv_len, a.page_table, a.max_pages, a.table_stride = kv_len.data_ptr(), page_table.data_ptr(), n, stride
-        a.B, a.S, a.HA, a.causal, a.scale = B, S, HA, int(bool(causal)), float(scale)
+        a = CsaCacheAttnArgs(q.data_ptr(), kc, vc, *pages, ip, topk, B, S, HA, bool(causal), scale, out.data_ptr(),
+                             lse.data_ptr() if lse is not None else None)
         if workspace is None:
-            need = csa_cache_attention_workspace_size(a)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws, size = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
-            if workspace is not None else (None, 0)
-        _check(csa_cache_attention(a, ws, size, ctypes.c_void_p(s.cuda_stream)), "csa_cache_attention")
-    return (out, lse) if return_lse else out
+            size = csa_cache_attention_workspace_size(a)
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+        else:
+            size = workspace.numel() * workspace.element_size()
+        _check(csa_cache_attention(a, workspace.data_ptr() if workspace is not None else None, size, s),
+               "csa_cache_attention")
+        return (out, lse) if return_lse else out
+
+    return _within(ctx, call, out, lse, workspace)

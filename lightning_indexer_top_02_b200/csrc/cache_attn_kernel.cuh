@@ -8,15 +8,17 @@
 //   O^T [16 dims x 8 rows] += V^T [16 x 16 keys] . P^T [16 keys x 8]
 // With at most 16 rows the work is bound by reading the cache (9/16 byte an
 // element against 4 rows' flops an element), so what matters is how few
-// instructions stand between the load of a code and its use.  The codes go from
-// global memory straight into registers in the layout of the MMA's A operand:
-// no shared memory, no transposition.
+// instructions stand between a code and its use.  A warp takes blocks of 32 keys;
+// their codes and scales come by cp.async two blocks ahead into the warp's own
+// staging rows and go from there into registers in the layout of the MMA's A
+// operand: no transposition, and no barrier between warps.
 //   K: the contraction's order is free, so thread (g, t) of a warp takes the
 //     16 * NG consecutive elements 16 * NG * t.. of the rows of its two keys --
 //     whole scale groups, one wide load -- and the query fragments are laid
 //     out to match.
-//   V: a key's order in the tile is free too: thread (g, t) reads rows
-//     4t .. 4t+3 of 16 keys, elements VU * g.. of each; two keys' codes of one
+//   V: a key's place in the tile is free too: thread (g, t) reads rows
+//     4t .. 4t+3 of 16 keys (two of them swapped for t > 1, which keeps the reads
+//     free of bank conflicts), elements VU * g.. of each; two keys' codes of one
 //     dimension are merged into a byte (one and-or for eight codes) that
 //     converts to the f16 pair that the A operand wants.
 //   P^T: the S^T accumulator holds (key g, rows 2t, 2t+1); movmatrix
@@ -50,6 +52,7 @@ using cache::PageMap;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlock = 32;                  // keys a warp takes at a time
+constexpr int kStages = 3;                  // blocks staged: one in use, two on their way
 constexpr float kLag = 8.0f;                // the maximum is raised past 2^8 only
 constexpr int kNoKey = 0x7FFFFFFF;          // a position no query sees
 
@@ -111,44 +114,92 @@ __device__ __forceinline__ int seen(const AttnParams &p, int len, int i)
     return p.causal ? len - p.S + i + 1 : len;
 }
 
-template <int N> struct Bytes { uint32_t w[(N + 3) / 4]; };
-
-// N bytes from an address aligned to the largest power of two dividing N (at most 16).
-template <int N>
-__device__ __forceinline__ Bytes<N> load_bytes(const uint8_t *src)
+// 16-byte piece q of a row among rows of kQ pieces: where it is staged, so that
+// eight rows' pieces q lie in eight different 16-byte places of a bank row.
+template <int kQ>
+__device__ __forceinline__ uint32_t staged_at(int r, int q)
 {
-    Bytes<N> r;
+    const int x = kQ == 2 ? (r >> 2) & 1 : kQ == 4 ? (r >> 1) & 3 : kQ == 8 ? r & 7 : 0;
+    return static_cast<uint32_t>((r * kQ + (q ^ x)) * 16);
+}
+
+__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+
+template <int kBytes>
+__device__ __forceinline__ void cp_async_small_zfill(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
+                 "r"(ok ? kBytes : 0)
+                 : "memory");
+}
+
+// Copies kRows rows of one operand to the warp's staging: a lane's piece is 16
+// bytes (32 elements) of a row.  Lane r < kRows holds row r's page (< 0: none, the
+// staged row is zeros) and row within the page.
+template <int kD, int kRows>
+__device__ __forceinline__ void stage_codes(const CacheView &c, uint32_t codes, int page, int row, int lane)
+{
+    constexpr int kQ = kD / 32, kN = kQ * kRows;          // pieces of a row, and in all
+    static_assert(kRows % 8 == 0, "eight lanes in a row take eight rows");
+#pragma unroll
+    for (int k = 0; k < (kN + 31) / 32; ++k) {
+        const int combo = 4 * k + (lane >> 3);
+        const int q = combo % kQ, r = (lane & 7) + 8 * (combo / kQ);
+        const int pg = __shfl_sync(0xffffffffu, page, r & (kRows - 1)), ro = __shfl_sync(0xffffffffu, row, r & (kRows - 1));
+        if (kN % 32 == 0 || combo < kN / 8)
+            cp_async_zfill(codes + staged_at<kQ>(r, q),
+                           c.data + static_cast<long long>(max(pg, 0)) * c.page_stride +
+                               static_cast<long long>(ro) * c.row_bytes + 16 * q,
+                           pg >= 0);
+    }
+}
+
+template <int kD>
+__device__ __forceinline__ void stage_scales(const CacheView &c, uint32_t scales, int r, int page, int row)
+{
+    constexpr int kS = kD / 16;                           // scale bytes of a row
+    const uint8_t *src = c.scale + static_cast<long long>(max(page, 0)) * c.scale_stride +
+                         static_cast<long long>(row) * c.scale_bytes;
+    if constexpr (kS == 16) {
+        cp_async_zfill(scales + r * kS, src, page >= 0);
+    } else if constexpr (kS == 8) {
+        cp_async_small_zfill<8>(scales + r * kS, src, page >= 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kS; j += 4)
+            cp_async_small_zfill<4>(scales + r * kS + j, src + j, page >= 0);
+    }
+}
+
+// N bytes of staged row r from byte `at` on (whole pieces, or within one; rows of
+// kQ = 6 pieces are staged as they are).
+template <int kQ, int N>
+__device__ __forceinline__ void read_staged(const uint8_t *rows, int r, int at, uint32_t (&w)[(N + 3) / 4])
+{
     if constexpr (N % 16 == 0) {
 #pragma unroll
         for (int j = 0; j < N / 16; ++j) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + j);
-            r.w[4 * j] = v.x;
-            r.w[4 * j + 1] = v.y;
-            r.w[4 * j + 2] = v.z;
-            r.w[4 * j + 3] = v.w;
+            const uint4 v = *reinterpret_cast<const uint4 *>(rows + staged_at<kQ>(r, (at >> 4) + j));
+            w[4 * j] = v.x;
+            w[4 * j + 1] = v.y;
+            w[4 * j + 2] = v.z;
+            w[4 * j + 3] = v.w;
         }
     } else if constexpr (N % 8 == 0) {
 #pragma unroll
         for (int j = 0; j < N / 8; ++j) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src) + j);
-            r.w[2 * j] = v.x;
-            r.w[2 * j + 1] = v.y;
+            const int b = at + 8 * j;
+            const uint2 v = *reinterpret_cast<const uint2 *>(rows + staged_at<kQ>(r, b >> 4) + (b & 15));
+            w[2 * j] = v.x;
+            w[2 * j + 1] = v.y;
         }
-    } else if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int j = 0; j < N / 4; ++j)
-            r.w[j] = __ldg(reinterpret_cast<const uint32_t *>(src) + j);
-    } else if constexpr (N == 2) {
-        r.w[0] = __ldg(reinterpret_cast<const uint16_t *>(src));
     } else {
-        static_assert(N < 4, "byte loads");
-        uint32_t v = 0;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            v |= static_cast<uint32_t>(__ldg(src + j)) << (8 * j);
-        r.w[0] = v;
+        static_assert(N == 4, "4, 8 or 16 bytes at a time");
+        w[0] = *reinterpret_cast<const uint32_t *>(rows + staged_at<kQ>(r, at >> 4) + (at & 15));
     }
-    return r;
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
@@ -199,41 +250,23 @@ struct Shape {
     static constexpr int NU = kDv / (8 * VU);            // and how many times
     static constexpr int MT = kDv / 16;                  // output m-tiles
     static constexpr int kRows = 8 * kNT;
-    static constexpr int kSmem = kWarps * kRows * (kDv + 2) * 4;
+    // staging of a block: K codes, V codes, K scales, V scales
+    static constexpr int kV = kBlock * kDk / 2, kKs = kV + kBlock * kDv / 2;
+    static constexpr int kVs = kKs + kBlock * kDk / 16, kStage = kVs + kBlock * kDv / 16;
+    // the warps' joined results take the staging's place
+    static constexpr int kJoin = kWarps * kRows * (kDv + 2) * 4, kStaging = kWarps * kStages * kStage;
+    static constexpr int kSmem = kJoin > kStaging ? kJoin : kStaging;
+    // blocks an SM holds: registers for O and the query, shared memory for the staging
+    static constexpr int kCtas = kDk + kDv <= 256 && kNT == 1 ? 4 : kDk + kDv <= 256 ? 3 : kDk + kDv <= 384 && kNT == 1 ? 3 : 2;
 };
-
-// The raw codes and scales of 32 keys, as this thread uses them.
-template <class Sh>
-struct Raw {
-    Bytes<8 * Sh::NG> k[4];                              // rows of the keys g, g+8 of two tiles
-    Bytes<Sh::NG> ks[4];
-    Bytes<Sh::VU / 2> v[8][Sh::NU];                      // rows 4t .. 4t+3 of two tiles
-    uint8_t vs[8][Sh::NU];
-    int pos;                                             // lane's key: its position (kNoKey: none)
-};
-
-// Position, page and row of the key in slot `slot` of a group.
-__device__ __forceinline__ void find_key(const AttnParams &p, const int32_t *list, const int32_t *table,
-                                         int slot, int last, int limit, int &pos, int &page, int &off)
-{
-    pos = kNoKey;
-    page = off = 0;
-    if (slot < last) {
-        const int s = list ? __ldg(list + slot) : slot;
-        if (s >= 0 && s < limit && p.pm.locate(table, s, page, off))
-            pos = s;
-        else
-            page = off = 0;
-    }
-}
 
 template <int kDk, int kDv, int kNT>
-__global__ void __launch_bounds__(kThreads, kNT == 1 && kDk + kDv <= 256 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
     cache_attn_kernel(const AttnParams p)
 {
     using Sh = Shape<kDk, kDv, kNT>;
     constexpr int NG = Sh::NG, VU = Sh::VU, NU = Sh::NU, MT = Sh::MT, RT = Sh::kRows;
-    extern __shared__ float smem[];                      // [warp][row][Dv + 2]
+    extern __shared__ __align__(16) uint8_t smem_raw[];  // staging, then [warp][row][Dv + 2]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int work = static_cast<int>(p.div_splits.div(blockIdx.x)), split = blockIdx.x - work * p.splits;
@@ -248,8 +281,9 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 && kDk + kDv <= 256 ? 3 : 2
     const int see_lo = len > 0 ? seen(p, len, gr.i0 + static_cast<int>(p.div_G.div(gr.r0))) : 0;
     const int slots = p.idx ? (see_hi > 0 ? p.topk : 0) : min(max(see_hi, 0), p.capacity);
     const int blocks = (slots + kBlock - 1) / kBlock;
-    const int b_lo = static_cast<int>(static_cast<long long>(blocks) * split / p.splits);
-    const int b_hi = static_cast<int>(static_cast<long long>(blocks) * (split + 1) / p.splits);
+    // even shares, the first ones a block larger
+    const int each = static_cast<int>(p.div_splits.div(blocks)), more = blocks - each * p.splits;
+    const int b_lo = each * split + min(split, more), b_hi = b_lo + each + (split < more ? 1 : 0);
 
     // query fragments: row g of each n-tile, elements 16 NG t.., scaled by a power of two
     uint32_t qf[kNT][4 * NG][2];
@@ -315,43 +349,65 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 && kDk + kDv <= 256 ? 3 : 2
                 o[j][n][c] = 0.0f;
     }
 
-    // rows of a tile of 16 keys: K rows k0, k0 + 2 (MMA rows g, g + 8), V rows 4t ..
-    const int k0 = 4 * (g >> 1) + (g & 1);
-    auto load = [&](int block, Raw<Sh> &raw) {
-        int page, off;
-        find_key(p, list, table, block * kBlock + lane, slots, see_hi, raw.pos, page, off);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = 16 * (j >> 1) + k0 + 2 * (j & 1);
-            const int pg = __shfl_sync(0xffffffffu, page, r), of = __shfl_sync(0xffffffffu, off, r);
-            raw.k[j] = load_bytes<8 * NG>(cache::row_data(p.ck, p.pm, pg, gr.h, of) + 8 * NG * t);
-            raw.ks[j] = load_bytes<NG>(cache::row_scale(p.ck, p.pm, pg, gr.h, of) + NG * t);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int r = 16 * (j >> 2) + 4 * t + (j & 3);
-            const int pg = __shfl_sync(0xffffffffu, page, r), of = __shfl_sync(0xffffffffu, off, r);
-            const int ok = __shfl_sync(0xffffffffu, raw.pos, r) != kNoKey;
-            const uint8_t *vd = cache::row_data(p.cv, p.pm, pg, gr.h, of) + (VU / 2) * g;
-            const uint8_t *vc = cache::row_scale(p.cv, p.pm, pg, gr.h, of) + (VU * g) / 16;
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                raw.v[j][u] = load_bytes<VU / 2>(vd + 4 * VU * u);
-                // a masked key's scale may be anything, NaN too: its P is zero, so its V is made zero
-                raw.vs[j][u] = ok ? __ldg(vc + (VU / 2) * u) : 0;
-            }
+    // rows of a tile of 16 keys: K rows k0, k0 + 2 (MMA rows g, g + 8), V rows 4t + (0, 1, 2, 3)
+    // with the pairs swapped for t > 1
+    const int k0 = 4 * (g >> 1) + ((g & 1) ^ (g >> 2));
+    const int v0 = 4 * t + (t >> 1), v1 = 4 * t + 1 - (t >> 1);
+    uint8_t *stage = smem_raw + warp * kStages * Sh::kStage;
+
+    // Three blocks ahead: the lane's position; the next: its page; two ahead: the
+    // copies.  Nothing that a load brought is looked at before the step that needs it.
+    int pos_f = kNoKey, pos_p = kNoKey, page_p = -1, row_p = 0;
+    auto fetch_pos = [&](int blk) {
+        pos_f = -1;
+        if (blk < b_hi) {
+            const int slot = blk * kBlock + lane;
+            if (slot < slots)
+                pos_f = list ? __ldg(list + slot) : slot;
         }
     };
-
-    Raw<Sh> raw;
+    auto fetch_page = [&]() {
+        const bool in = pos_f >= 0 && pos_f < see_hi;
+        const int n = in ? static_cast<int>(p.pm.div.div(pos_f)) : 0;
+        const bool has = in && n < p.pm.max_pages;
+        page_p = has ? __ldg(table + n) : -1;
+        row_p = gr.h * p.pm.page_size + (has ? pos_f - n * p.pm.page_size : 0);
+        pos_p = has ? pos_f : kNoKey;
+    };
+    // starts a block's copies; returns the lane's position in it (kNoKey: none)
+    auto start = [&](int blk, int at) -> int {
+        int pos = kNoKey;
+        if (blk < b_hi) {
+            const int page = page_p >= 0 && page_p < p.pm.num_pages ? page_p : -1;
+            pos = page >= 0 ? pos_p : kNoKey;
+            const uint32_t to = smem_u32(stage + at * Sh::kStage);
+            stage_codes<kDk, kBlock>(p.ck, to, page, row_p, lane);
+            stage_codes<kDv, kBlock>(p.cv, to + Sh::kV, page, row_p, lane);
+            stage_scales<kDk>(p.ck, to + Sh::kKs, lane, page, row_p);
+            stage_scales<kDv>(p.cv, to + Sh::kVs, lane, page, row_p);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return pos;
+    };
     int blk = b_lo + warp;
-    if (blk < b_hi)
-        load(blk, raw);
-    while (blk < b_hi) {
-        const Raw<Sh> cur = raw;
-        const int next = blk + kWarps;
-        if (next < b_hi)
-            load(next, raw);
+    fetch_pos(blk);
+    fetch_page();
+    fetch_pos(blk + kWarps);
+    int pos0 = start(blk, 0);
+    fetch_page();
+    fetch_pos(blk + 2 * kWarps);
+    int pos1 = start(blk + kWarps, 1);
+    fetch_page();
+    fetch_pos(blk + 3 * kWarps);
+    for (int at = 0, to = 2; blk < b_hi; blk += kWarps) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");   // this block's have landed
+        __syncwarp();                                          // every lane's; and the stage before is free
+        const int pos2 = start(blk + 2 * kWarps, to);
+        fetch_page();
+        fetch_pos(blk + 4 * kWarps);
+        const uint8_t *cur = stage + at * Sh::kStage;
+        at = at == kStages - 1 ? 0 : at + 1;
+        to = to == kStages - 1 ? 0 : to + 1;
         // S^T of two tiles of 16 keys
         float s[2][kNT][4];
 #pragma unroll
@@ -361,37 +417,44 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 && kDk + kDv <= 256 ? 3 : 2
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     s[a][n][c] = 0.0f;
+            // the thread's parts of its two rows
+            uint32_t kw[2][2 * NG], sc[2][NG];
 #pragma unroll
-            for (int c = 0; c < NG; ++c) {
-                // the group's scale in both halves
-                uint32_t sc[2];
+            for (int e = 0; e < 2; ++e) {
+                const int r = 16 * a + k0 + 2 * e;
+                read_staged<kDk / 32, 8 * NG>(cur, r, 8 * NG * t, kw[e]);
+                const uint8_t *s8 = cur + Sh::kKs + r * (kDk / 16) + NG * t;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t byte = cur.ks[2 * a + e].w[0] >> (8 * c) & 0xFFu;
-                    sc[e] = cache::f16x2_of_e4m3x2(byte * 0x0101u);
+                for (int c = 0; c < NG; c += 2) {             // scales, each in both halves
+                    const uint32_t two = cache::f16x2_of_e4m3x2(
+                        NG % 2 == 0 ? *reinterpret_cast<const uint16_t *>(s8 + c) : s8[c] | (c + 1 < NG ? s8[c + 1] << 8 : 0));
+                    sc[e][c] = __byte_perm(two, 0u, 0x1010);
+                    if (c + 1 < NG)
+                        sc[e][c + 1] = __byte_perm(two, 0u, 0x3232);
                 }
+            }
+#pragma unroll
+            for (int c = 0; c < NG; ++c)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const uint32_t w0 = cur.k[2 * a].w[2 * c + (q >> 1)];
-                    const uint32_t w1 = cur.k[2 * a + 1].w[2 * c + (q >> 1)];
+                    const uint32_t w0 = kw[0][2 * c + (q >> 1)], w1 = kw[1][2 * c + (q >> 1)];
                     const int j = 2 * (q & 1);
-                    const uint32_t a0 = hmul2(pair_of(w0, j), sc[0]), a2 = hmul2(pair_of(w0, j + 1), sc[0]);
-                    const uint32_t a1 = hmul2(pair_of(w1, j), sc[1]), a3 = hmul2(pair_of(w1, j + 1), sc[1]);
+                    const uint32_t a0 = hmul2(pair_of(w0, j), sc[0][c]), a2 = hmul2(pair_of(w0, j + 1), sc[0][c]);
+                    const uint32_t a1 = hmul2(pair_of(w1, j), sc[1][c]), a3 = hmul2(pair_of(w1, j + 1), sc[1][c]);
 #pragma unroll
                     for (int n = 0; n < kNT; ++n)
                         mma16816(s[a][n], a0, a1, a2, a3, qf[n][4 * c + q][0], qf[n][4 * c + q][1]);
                 }
-            }
         }
         // masks: the positions of the thread's four keys
-        const bool whole = __all_sync(0xffffffffu, cur.pos < see_lo);
+        const bool whole = __all_sync(0xffffffffu, pos0 < see_lo);
         int kp[2][2];
         if (!whole) {
 #pragma unroll
             for (int a = 0; a < 2; ++a)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    kp[a][e] = __shfl_sync(0xffffffffu, cur.pos, 16 * a + k0 + 2 * e);
+                    kp[a][e] = __shfl_sync(0xffffffffu, pos0, 16 * a + k0 + 2 * e);
         }
         bool raise = false;
         float top[kNT][2];
@@ -456,16 +519,22 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 && kDk + kDv <= 256 ? 3 : 2
         for (int a = 0; a < 2; ++a)
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
-                uint32_t sc[2];
+                uint32_t vw[4][VU / 8], sc[2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    read_staged<kDv / 32, VU / 2>(cur + Sh::kV, 16 * a + ((e & 1) ? v1 : v0) + (e & 2), 4 * VU * u + (VU / 2) * g,
+                                                  vw[e]);
+                const uint8_t *s8 = cur + Sh::kVs + (VU / 2) * u + (VU * g) / 16;
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    sc[e] = cache::f16x2_of_e4m3x2(cur.vs[4 * a + 2 * e][u] | cur.vs[4 * a + 2 * e + 1][u] << 8);
+                    sc[e] = cache::f16x2_of_e4m3x2(s8[(16 * a + v0 + 2 * e) * (kDv / 16)] |
+                                                   s8[(16 * a + v1 + 2 * e) * (kDv / 16)] << 8);
 #pragma unroll
                 for (int w = 0; w < VU / 8; ++w) {
                     uint32_t lo[2], hi[2];              // even and odd dimensions, a byte = two keys
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t x = cur.v[4 * a + 2 * e][u].w[w], y = cur.v[4 * a + 2 * e + 1][u].w[w];
+                        const uint32_t x = vw[2 * e][w], y = vw[2 * e + 1][w];
                         lo[e] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
                         hi[e] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
                     }
@@ -479,10 +548,14 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 && kDk + kDv <= 256 ? 3 : 2
                     }
                 }
             }
-        blk = next;
+        pos0 = pos1;
+        pos1 = pos2;
     }
+    cp_async_wait_all();
+    __syncthreads();                                     // the staging becomes the join's buffer
 
     // join the warps: every warp's O, maxima and sums go to shared memory
+    float *smem = reinterpret_cast<float *>(smem_raw);
     float *mine = smem + warp * RT * (kDv + 2);
 #pragma unroll
     for (int n = 0; n < kNT; ++n)

@@ -123,66 +123,6 @@ __device__ __forceinline__ Item item_of(const AttnParams &p, int item, int tile_
 
 // ---------------------------------------------------------------- gather
 
-// 16-byte piece q of a row among rows of kQ pieces: where it is staged, so that
-// eight rows' pieces q lie in eight different 16-byte places of a bank row.
-template <int kQ>
-__device__ __forceinline__ uint32_t staged_at(int r, int q)
-{
-    const int x = kQ == 2 ? (r >> 2) & 1 : kQ == 4 ? (r >> 1) & 3 : kQ == 8 ? r & 7 : 0;
-    return static_cast<uint32_t>((r * kQ + (q ^ x)) * 16);
-}
-
-__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void *src, bool ok)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-
-template <int kBytes>
-__device__ __forceinline__ void cp_async_small_zfill(uint32_t dst, const void *src, bool ok)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
-                 "r"(ok ? kBytes : 0)
-                 : "memory");
-}
-
-// Copies kRows rows of one operand to the warp's staging: a lane's piece is 16
-// bytes (32 elements) of a row.  Lane r < kRows holds row r's page (< 0: none, the
-// staged row is zeros) and row within the page.
-template <int kD, int kRows>
-__device__ __forceinline__ void stage_codes(const CacheView &c, uint32_t codes, int page, int row, int lane)
-{
-    constexpr int kQ = kD / 32, kN = kQ * kRows;          // pieces of a row, and in all
-    static_assert(kRows % 8 == 0, "eight lanes in a row take eight rows");
-#pragma unroll
-    for (int k = 0; k < (kN + 31) / 32; ++k) {
-        const int combo = 4 * k + (lane >> 3);
-        const int q = combo % kQ, r = (lane & 7) + 8 * (combo / kQ);
-        const int pg = __shfl_sync(0xffffffffu, page, r & (kRows - 1)), ro = __shfl_sync(0xffffffffu, row, r & (kRows - 1));
-        if (kN % 32 == 0 || combo < kN / 8)
-            cp_async_zfill(codes + staged_at<kQ>(r, q),
-                           c.data + static_cast<long long>(max(pg, 0)) * c.page_stride +
-                               static_cast<long long>(ro) * c.row_bytes + 16 * q,
-                           pg >= 0);
-    }
-}
-
-template <int kD>
-__device__ __forceinline__ void stage_scales(const CacheView &c, uint32_t scales, int r, int page, int row)
-{
-    constexpr int kS = kD / 16;                           // scale bytes of a row
-    const uint8_t *src = c.scale + static_cast<long long>(max(page, 0)) * c.scale_stride +
-                         static_cast<long long>(row) * c.scale_bytes;
-    if constexpr (kS == 16) {
-        cp_async_zfill(scales + r * kS, src, page >= 0);
-    } else if constexpr (kS == 8) {
-        cp_async_small_zfill<8>(scales + r * kS, src, page >= 0);
-    } else {
-#pragma unroll
-        for (int j = 0; j < kS; j += 4)
-            cp_async_small_zfill<4>(scales + r * kS + j, src + j, page >= 0);
-    }
-}
-
 // Converts staged rows to an operand stage: element e of tile row r goes to
 // stage + (e / 64) * kKeys * 128 + r * 128 + ((e / 8 % 8) ^ (r & 7)) * 16.  Eight
 // lanes in a row store the same unit of eight different tile rows, whose swizzled

@@ -444,7 +444,7 @@ def test_workspace(lib):
     for _ in range(2):
         assert torch.equal(L.cache_attention(q, c, c, table, lens, scale=0.09, workspace=ws), want)
     a = L.cache.CsaCacheAttnArgs()                                              # and without one: stream-ordered
-    a.cache_k = a.cache_v = L.cache._cache_struct("c", c, q.device)
+    a.cache_k = a.cache_v = L.cache._cache_struct("c", c)
     out = torch.empty((1, 1, 8, 128), dtype=torch.bfloat16, device="cuda")
     a.q, a.out, a.kv_len, a.page_table = q.data_ptr(), out.data_ptr(), lens.data_ptr(), table.data_ptr()
     a.max_pages = a.table_stride = 64
