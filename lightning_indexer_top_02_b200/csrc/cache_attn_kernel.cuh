@@ -35,9 +35,17 @@
 // move 4 bytes an element for each 9/16 byte that memory delivers, more than
 // shared memory's 128 bytes a clock allow at the memory's rate.
 //
-// Warps take blocks of 32 keys of a block's share of the keys in turn and
-// keep their own running maxima, sums and O; they are joined in shared
-// memory at the end, and the shares of one tile by a second kernel.
+// Where every key is read and pages hold whole tiles of 16 keys (kBulk), a tile is
+// 16 rows of one page, and eight lanes fetch a block's eight pieces with one bulk
+// copy each; else every row is found by itself and copied 16 bytes at a time, which
+// takes about 150 instructions more of some 750 a block.
+//
+// The CTAs that the GPU holds share out all the chunks of 128 keys of all row tiles,
+// evenly and in order, whatever the sequences' lengths: a CTA's share is a run of
+// chunks, which ends one tile, takes whole ones and begins another.  In a tile the
+// warps take blocks of 32 keys in turn and keep their own running maxima, sums and O,
+// which are joined in shared memory; the pieces of a tile that several CTAs share
+// are joined by a second kernel.
 #pragma once
 #include "cache_common.cuh"
 #include "ptx.cuh"
@@ -52,6 +60,7 @@ using cache::PageMap;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlock = 32;                  // keys a warp takes at a time
+constexpr int kChunk = kBlock * kWarps;     // keys that are shared out together
 constexpr int kStages = 3;                  // blocks staged: one in use, two on their way
 constexpr float kLag = 8.0f;                // the maximum is raised past 2^8 only
 constexpr int kNoKey = 0x7FFFFFFF;          // a position no query sees
@@ -69,11 +78,14 @@ struct AttnParams {
     float v_scale;
     __nv_bfloat16 *out;
     float *lse;
-    int splits;                             // shares of the keys
+    long long wait_limit;
+    int splits;                             // wide kernel: shares of the keys
+    int ctas;                               // CTAs that share the chunks; 0: one a row tile (at most a chunk each)
+    int works;                              // row tiles of a sequence
     int tiles;                              // row tiles of a group
     int rows;                               // query rows of a group: S * G, or G with idx
     int capacity;                           // positions the page table reaches
-    float *part;                            // [work][split][rows of a tile][Dv + 2]
+    float *part;                            // [piece][rows of a tile][Dv + 2]
     FastDiv div_splits, div_tiles, div_H, div_S, div_G;
 };
 
@@ -137,10 +149,10 @@ __device__ __forceinline__ void cp_async_small_zfill(uint32_t dst, const void *s
 }
 
 // Copies kRows rows of one operand to the warp's staging: a lane's piece is 16
-// bytes (32 elements) of a row.  Lane r < kRows holds row r's page (< 0: none, the
-// staged row is zeros) and row within the page.
+// bytes (32 elements) of a row.  Lane r < kRows holds row r's address; rows whose bit in
+// `has` is clear are staged as zeros.
 template <int kD, int kRows>
-__device__ __forceinline__ void stage_codes(const CacheView &c, uint32_t codes, int page, int row, int lane)
+__device__ __forceinline__ void stage_codes(uint32_t codes, const uint8_t *row, uint32_t has, int lane)
 {
     constexpr int kQ = kD / 32, kN = kQ * kRows;          // pieces of a row, and in all
     static_assert(kRows % 8 == 0, "eight lanes in a row take eight rows");
@@ -148,41 +160,62 @@ __device__ __forceinline__ void stage_codes(const CacheView &c, uint32_t codes, 
     for (int k = 0; k < (kN + 31) / 32; ++k) {
         const int combo = 4 * k + (lane >> 3);
         const int q = combo % kQ, r = (lane & 7) + 8 * (combo / kQ);
-        const int pg = __shfl_sync(0xffffffffu, page, r & (kRows - 1)), ro = __shfl_sync(0xffffffffu, row, r & (kRows - 1));
+        const uint8_t *src = reinterpret_cast<const uint8_t *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r & (kRows - 1)));
         if (kN % 32 == 0 || combo < kN / 8)
-            cp_async_zfill(codes + staged_at<kQ>(r, q),
-                           c.data + static_cast<long long>(max(pg, 0)) * c.page_stride +
-                               static_cast<long long>(ro) * c.row_bytes + 16 * q,
-                           pg >= 0);
+            cp_async_zfill(codes + staged_at<kQ>(r, q), src + 16 * q, has >> r & 1u);
     }
 }
 
 template <int kD>
-__device__ __forceinline__ void stage_scales(const CacheView &c, uint32_t scales, int r, int page, int row)
+__device__ __forceinline__ void stage_scales(uint32_t scales, int r, const uint8_t *src, bool ok)
 {
     constexpr int kS = kD / 16;                           // scale bytes of a row
-    const uint8_t *src = c.scale + static_cast<long long>(max(page, 0)) * c.scale_stride +
-                         static_cast<long long>(row) * c.scale_bytes;
     if constexpr (kS == 16) {
-        cp_async_zfill(scales + r * kS, src, page >= 0);
+        cp_async_zfill(scales + r * kS, src, ok);
     } else if constexpr (kS == 8) {
-        cp_async_small_zfill<8>(scales + r * kS, src, page >= 0);
+        cp_async_small_zfill<8>(scales + r * kS, src, ok);
     } else {
 #pragma unroll
         for (int j = 0; j < kS; j += 4)
-            cp_async_small_zfill<4>(scales + r * kS + j, src + j, page >= 0);
+            cp_async_small_zfill<4>(scales + r * kS + j, src + j, ok);
     }
 }
 
+// Addresses of row `row` (head * page_size + offset) of a page; page < 0: of page 0.
+__device__ __forceinline__ const uint8_t *data_at(const CacheView &c, int page, int row)
+{
+    return c.data + max(page, 0) * c.page_stride + static_cast<long long>(row) * c.row_bytes;
+}
+
+__device__ __forceinline__ const uint8_t *scale_at(const CacheView &c, int page, int row)
+{
+    return c.scale + max(page, 0) * c.scale_stride + static_cast<long long>(row) * c.scale_bytes;
+}
+
+// 16 * n bytes global -> shared by the copy engine, counted on `bar`.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 // N bytes of staged row r from byte `at` on (whole pieces, or within one; rows of
-// kQ = 6 pieces are staged as they are).
-template <int kQ, int N>
+// kQ = 6 pieces, and bulk copies, are staged as they are).
+template <int kQ, bool kBulk>
+__device__ __forceinline__ uint32_t staged(int r, int q)
+{
+    return kBulk ? static_cast<uint32_t>((r * kQ + q) * 16) : staged_at<kQ>(r, q);
+}
+
+template <int kQ, int N, bool kBulk>
 __device__ __forceinline__ void read_staged(const uint8_t *rows, int r, int at, uint32_t (&w)[(N + 3) / 4])
 {
     if constexpr (N % 16 == 0) {
 #pragma unroll
         for (int j = 0; j < N / 16; ++j) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(rows + staged_at<kQ>(r, (at >> 4) + j));
+            const uint4 v = *reinterpret_cast<const uint4 *>(rows + staged<kQ, kBulk>(r, (at >> 4) + j));
             w[4 * j] = v.x;
             w[4 * j + 1] = v.y;
             w[4 * j + 2] = v.z;
@@ -192,13 +225,13 @@ __device__ __forceinline__ void read_staged(const uint8_t *rows, int r, int at, 
 #pragma unroll
         for (int j = 0; j < N / 8; ++j) {
             const int b = at + 8 * j;
-            const uint2 v = *reinterpret_cast<const uint2 *>(rows + staged_at<kQ>(r, b >> 4) + (b & 15));
+            const uint2 v = *reinterpret_cast<const uint2 *>(rows + staged<kQ, kBulk>(r, b >> 4) + (b & 15));
             w[2 * j] = v.x;
             w[2 * j + 1] = v.y;
         }
     } else {
         static_assert(N == 4, "4, 8 or 16 bytes at a time");
-        w[0] = *reinterpret_cast<const uint32_t *>(rows + staged_at<kQ>(r, at >> 4) + (at & 15));
+        w[0] = *reinterpret_cast<const uint32_t *>(rows + staged<kQ, kBulk>(r, at >> 4) + (at & 15));
     }
 }
 
@@ -255,375 +288,632 @@ struct Shape {
     static constexpr int kVs = kKs + kBlock * kDk / 16, kStage = kVs + kBlock * kDv / 16;
     // the warps' joined results take the staging's place
     static constexpr int kJoin = kWarps * kRows * (kDv + 2) * 4, kStaging = kWarps * kStages * kStage;
-    static constexpr int kSmem = kJoin > kStaging ? kJoin : kStaging;
+    static constexpr int kBars = kJoin > kStaging ? kJoin : kStaging;    // barriers, abort flag
+    static constexpr int kSmem = kBars + kWarps * kStages * 8 + 16;
     // blocks an SM holds: registers for O and the query, shared memory for the staging
     static constexpr int kCtas = kDk + kDv <= 256 && kNT == 1 ? 4 : kDk + kDv <= 256 ? 3 : kDk + kDv <= 384 && kNT == 1 ? 3 : 2;
 };
 
-template <int kDk, int kDv, int kNT>
+// Chunks of one row tile of sequence b.  (A tile of early queries sees less of the
+// sequence; the chunks past that find nothing to do.)
+__device__ __forceinline__ int chunks_of(const AttnParams &p, int b)
+{
+    const int len = __ldg(p.kv_len + b);
+    const int n = len > 0 ? (p.idx ? p.topk : min(len, p.capacity)) : 0;
+    return static_cast<int>((static_cast<unsigned>(n) + kChunk - 1) / kChunk);
+}
+
+// Sum over the block's kThreads threads (scratch: kWarps words).
+__device__ __forceinline__ long long block_sum(long long v, long long *scratch)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, d);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return scratch[0] + scratch[1] + scratch[2] + scratch[3];
+}
+static_assert(kWarps == 4, "block_sum");
+
+// Chunks of the sequences before `upto`.
+__device__ __forceinline__ long long chunks_before(const AttnParams &p, int upto, long long *scratch)
+{
+    long long v = 0;
+    for (int b = threadIdx.x; b < upto; b += kThreads)
+        v += chunks_of(p, b);
+    return block_sum(v, scratch) * p.works;
+}
+
+// The sequence that holds chunk x of all, and x's place in it (found: shared memory).
+struct Found {
+    int b;
+    long long y;
+};
+
+__device__ __forceinline__ void find_chunk(const AttnParams &p, long long x, Found *found, long long *scratch)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    long long carry = 0;
+    for (int base = 0; base < p.B; base += kThreads) {
+        const int b = base + threadIdx.x;
+        const long long v = b < p.B ? static_cast<long long>(chunks_of(p, b)) * p.works : 0;
+        long long upto = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, upto, d);
+            upto += lane >= d ? u : 0;
+        }
+        __syncthreads();
+        if (lane == 31)
+            scratch[warp] = upto;
+        __syncthreads();
+        long long start = carry + upto - v;
+        for (int w = 0; w < kWarps; ++w) {
+            start += w < warp ? scratch[w] : 0;
+            carry += scratch[w];
+        }
+        if (x >= start && x < start + v) {
+            found->b = b;
+            found->y = x - start;
+        }
+    }
+    __syncthreads();
+}
+
+// The CTA whose share holds chunk x of `total`: shares start at total * k / ctas.
+__device__ __forceinline__ int cta_of(long long x, long long total, int ctas)
+{
+    return static_cast<int>(((x + 1) * ctas - 1) / total);
+}
+
+template <int kDk, int kDv, int kNT, bool kBulk>
 __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
     cache_attn_kernel(const AttnParams p)
 {
     using Sh = Shape<kDk, kDv, kNT>;
     constexpr int NG = Sh::NG, VU = Sh::VU, NU = Sh::NU, MT = Sh::MT, RT = Sh::kRows;
     extern __shared__ __align__(16) uint8_t smem_raw[];  // staging, then [warp][row][Dv + 2]
+    __shared__ long long scratch[kWarps];
+    __shared__ Found found;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int work = static_cast<int>(p.div_splits.div(blockIdx.x)), split = blockIdx.x - work * p.splits;
-    const Group gr = group_of(p, work, RT);
-    const int len = __ldg(p.kv_len + gr.b);
-    const int32_t *table = p.pm.table + gr.b * p.pm.table_stride;
-    const int32_t *list = p.idx ? p.idx + (static_cast<long long>(gr.b) * p.S + gr.i0) * p.topk : nullptr;
-
-    // the tile's rows: what the last and the first of them see
-    const int r_last = min(gr.r0 + RT, p.rows) - 1;
-    const int see_hi = len > 0 ? seen(p, len, gr.i0 + static_cast<int>(p.div_G.div(r_last))) : 0;
-    const int see_lo = len > 0 ? seen(p, len, gr.i0 + static_cast<int>(p.div_G.div(gr.r0))) : 0;
-    const int slots = p.idx ? (see_hi > 0 ? p.topk : 0) : min(max(see_hi, 0), p.capacity);
-    const int blocks = (slots + kBlock - 1) / kBlock;
-    // even shares, the first ones a block larger
-    const int each = static_cast<int>(p.div_splits.div(blocks)), more = blocks - each * p.splits;
-    const int b_lo = each * split + min(split, more), b_hi = b_lo + each + (split < more ? 1 : 0);
-
-    // query fragments: row g of each n-tile, elements 16 NG t.., scaled by a power of two
-    uint32_t qf[kNT][4 * NG][2];
-    float f[kNT][2];                                     // factor of rows 2t, 2t+1 (log2 domain)
-    int lim[kNT][2];                                     // and the positions they see
-#pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-        const int r = gr.r0 + 8 * n + g;
-        float x[16 * NG];
-        float peak = 0.0f;
-        int i = 0, head = 0;
-        if (r < p.rows) {
-            row_of(p, gr, r, i, head);
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                p.q + ((static_cast<long long>(gr.b) * p.S + i) * p.HA + head) * kDk + 16 * NG * t);
-#pragma unroll
-            for (int j = 0; j < 2 * NG; ++j) {
-                const uint4 w = __ldg(src + j);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 v = cache::float2_of_bf16x2(u[e]);
-                    x[8 * j + 2 * e] = v.x;
-                    x[8 * j + 2 * e + 1] = v.y;
-                    peak = fmaxf(peak, fmaxf(fabsf(v.x), fabsf(v.y)));
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16 * NG; ++j)
-                x[j] = 0.0f;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_raw + Sh::kBars) + warp * kStages;
+    int *abort = reinterpret_cast<int *>(smem_raw + Sh::kBars + kWarps * kStages * 8);
+    const WaitCtl ctl{abort, p.wait_limit};
+    if constexpr (kBulk) {
+        if (lane == 0) {
+            for (int s = 0; s < kStages; ++s)
+                mbar_init(&bars[s], 1);
+            fence_mbar_init();
         }
-        peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
-        peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
-        // exponents of the scale and of its inverse, both normal powers of two
-        const int e = min(max(static_cast<int>(__float_as_uint(peak) >> 23), 1), 253);
-        const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-        const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
-#pragma unroll
-        for (int s = 0; s < 4 * NG; ++s) {
-            qf[n][s][0] = f16x2_of(x[4 * s] * down, x[4 * s + 1] * down);
-            qf[n][s][1] = f16x2_of(x[4 * s + 2] * down, x[4 * s + 3] * down);
+        if (threadIdx.x == 0)
+            *abort = 0;
+    }
+    __syncthreads();
+    // the CTA's share: `left` chunks from chunk y of sequence `seq` on
+    long long left = 1, y = 0;
+    int seq = 0;
+    if (p.ctas) {
+        const long long total = chunks_before(p, p.B, scratch);
+        const int ctas = static_cast<int>(min(static_cast<long long>(p.ctas), total));   // no share is empty
+        left = 0;
+        if (blockIdx.x < ctas) {
+            const long long x = total * blockIdx.x / ctas;
+            left = total * (blockIdx.x + 1) / ctas - x;
+            find_chunk(p, x, &found, scratch);
+            seq = found.b;
+            y = found.y;
         }
-        const float fr = up * p.sl2;
-        const int see = r < p.rows && len > 0 ? seen(p, len, i) : 0;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            f[n][c] = __shfl_sync(0xffffffffu, fr, 4 * (2 * t + c));
-            lim[n][c] = __shfl_sync(0xffffffffu, see, 4 * (2 * t + c));
+        // sequences without a key: zeros
+        for (int b = blockIdx.x; b < p.B; b += p.ctas) {
+            if (chunks_of(p, b) > 0)
+                continue;
+            const long long at = static_cast<long long>(b) * p.S * p.HA, n = static_cast<long long>(p.S) * p.HA;
+            for (long long e = threadIdx.x; e < n * (kDv / 8); e += kThreads)
+                reinterpret_cast<uint4 *>(p.out + at * kDv)[e] = make_uint4(0u, 0u, 0u, 0u);
+            for (long long e = threadIdx.x; p.lse && e < n; e += kThreads)
+                p.lse[at + e] = -INFINITY;
         }
     }
-
-    float o[MT][kNT][4];
-    float m[kNT][2], l[kNT][2];
-#pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-        m[n][0] = m[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                o[j][n][c] = 0.0f;
-    }
-
-    // rows of a tile of 16 keys: K rows k0, k0 + 2 (MMA rows g, g + 8), V rows 4t + (0, 1, 2, 3)
-    // with the pairs swapped for t > 1
-    const int k0 = 4 * (g >> 1) + ((g & 1) ^ (g >> 2));
-    const int v0 = 4 * t + (t >> 1), v1 = 4 * t + 1 - (t >> 1);
-    uint8_t *stage = smem_raw + warp * kStages * Sh::kStage;
-
-    // Three blocks ahead: the lane's position; the next: its page; two ahead: the
-    // copies.  Nothing that a load brought is looked at before the step that needs it.
-    int pos_f = kNoKey, pos_p = kNoKey, page_p = -1, row_p = 0;
-    auto fetch_pos = [&](int blk) {
-        pos_f = -1;
-        if (blk < b_hi) {
-            const int slot = blk * kBlock + lane;
-            if (slot < slots)
-                pos_f = list ? __ldg(list + slot) : slot;
-        }
-    };
-    auto fetch_page = [&]() {
-        const bool in = pos_f >= 0 && pos_f < see_hi;
-        const int n = in ? static_cast<int>(p.pm.div.div(pos_f)) : 0;
-        const bool has = in && n < p.pm.max_pages;
-        page_p = has ? __ldg(table + n) : -1;
-        row_p = gr.h * p.pm.page_size + (has ? pos_f - n * p.pm.page_size : 0);
-        pos_p = has ? pos_f : kNoKey;
-    };
-    // starts a block's copies; returns the lane's position in it (kNoKey: none)
-    auto start = [&](int blk, int at) -> int {
-        int pos = kNoKey;
-        if (blk < b_hi) {
-            const int page = page_p >= 0 && page_p < p.pm.num_pages ? page_p : -1;
-            pos = page >= 0 ? pos_p : kNoKey;
-            const uint32_t to = smem_u32(stage + at * Sh::kStage);
-            stage_codes<kDk, kBlock>(p.ck, to, page, row_p, lane);
-            stage_codes<kDv, kBlock>(p.cv, to + Sh::kV, page, row_p, lane);
-            stage_scales<kDk>(p.ck, to + Sh::kKs, lane, page, row_p);
-            stage_scales<kDv>(p.cv, to + Sh::kVs, lane, page, row_p);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        return pos;
-    };
-    int blk = b_lo + warp;
-    fetch_pos(blk);
-    fetch_page();
-    fetch_pos(blk + kWarps);
-    int pos0 = start(blk, 0);
-    fetch_page();
-    fetch_pos(blk + 2 * kWarps);
-    int pos1 = start(blk + kWarps, 1);
-    fetch_page();
-    fetch_pos(blk + 3 * kWarps);
-    for (int at = 0, to = 2; blk < b_hi; blk += kWarps) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");   // this block's have landed
-        __syncwarp();                                          // every lane's; and the stage before is free
-        const int pos2 = start(blk + 2 * kWarps, to);
-        fetch_page();
-        fetch_pos(blk + 4 * kWarps);
-        const uint8_t *cur = stage + at * Sh::kStage;
-        at = at == kStages - 1 ? 0 : at + 1;
-        to = to == kStages - 1 ? 0 : to + 1;
-        // S^T of two tiles of 16 keys
-        float s[2][kNT][4];
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-#pragma unroll
-            for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    s[a][n][c] = 0.0f;
-            // the thread's parts of its two rows
-            uint32_t kw[2][2 * NG], sc[2][NG];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 16 * a + k0 + 2 * e;
-                read_staged<kDk / 32, 8 * NG>(cur, r, 8 * NG * t, kw[e]);
-                const uint8_t *s8 = cur + Sh::kKs + r * (kDk / 16) + NG * t;
-#pragma unroll
-                for (int c = 0; c < NG; c += 2) {             // scales, each in both halves
-                    const uint32_t two = cache::f16x2_of_e4m3x2(
-                        NG % 2 == 0 ? *reinterpret_cast<const uint16_t *>(s8 + c) : s8[c] | (c + 1 < NG ? s8[c + 1] << 8 : 0));
-                    sc[e][c] = __byte_perm(two, 0u, 0x1010);
-                    if (c + 1 < NG)
-                        sc[e][c + 1] = __byte_perm(two, 0u, 0x3232);
-                }
+    uint32_t phase = 0;                                  // of the staging barriers
+    int at = 0;                                          // stage of the next block
+    while (left > 0) {
+        int work = blockIdx.x, lo = 0, hi = 1, all = 1;      // the segment: chunks lo .. hi - 1 of `all`
+        if (p.ctas) {
+            all = chunks_of(p, seq);
+            const int w = static_cast<int>(y / all);
+            lo = static_cast<int>(y - static_cast<long long>(w) * all);
+            hi = static_cast<int>(min(static_cast<long long>(all), lo + left));
+            work = seq * p.works + w;
+            y += hi - lo;
+            if (y == static_cast<long long>(all) * p.works) {
+                y = 0;
+                do
+                    ++seq;
+                while (seq < p.B && chunks_of(p, seq) == 0);
             }
+        }
+        left -= hi - lo;
+        const Group gr = group_of(p, work, RT);
+        const int len = __ldg(p.kv_len + gr.b);
+        const int32_t *table = p.pm.table + gr.b * p.pm.table_stride;
+        const int32_t *list = p.idx ? p.idx + (static_cast<long long>(gr.b) * p.S + gr.i0) * p.topk : nullptr;
+
+        // the tile's rows: what the last and the first of them see
+        const int r_last = min(gr.r0 + RT, p.rows) - 1;
+        const int see_hi = len > 0 ? seen(p, len, gr.i0 + static_cast<int>(p.div_G.div(r_last))) : 0;
+        const int see_lo = len > 0 ? seen(p, len, gr.i0 + static_cast<int>(p.div_G.div(gr.r0))) : 0;
+        const int slots = p.idx ? (see_hi > 0 ? p.topk : 0) : min(max(see_hi, 0), p.capacity);
+        const int blocks = (slots + kBlock - 1) / kBlock;
+        const int b_lo = lo * (kChunk / kBlock), b_hi = min(hi * (kChunk / kBlock), blocks);
+
+        // query fragments: row g of each n-tile, elements 16 NG t.., scaled by a power of two
+        uint32_t qf[kNT][4 * NG][2];
+        float f[kNT][2];                                     // factor of rows 2t, 2t+1 (log2 domain)
+        int lim[kNT][2];                                     // and the positions they see
 #pragma unroll
-            for (int c = 0; c < NG; ++c)
+        for (int n = 0; n < kNT; ++n) {
+            const int r = gr.r0 + 8 * n + g;
+            float x[16 * NG];
+            float peak = 0.0f;
+            int i = 0, head = 0;
+            if (r < p.rows) {
+                row_of(p, gr, r, i, head);
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    p.q + ((static_cast<long long>(gr.b) * p.S + i) * p.HA + head) * kDk + 16 * NG * t);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t w0 = kw[0][2 * c + (q >> 1)], w1 = kw[1][2 * c + (q >> 1)];
-                    const int j = 2 * (q & 1);
-                    const uint32_t a0 = hmul2(pair_of(w0, j), sc[0][c]), a2 = hmul2(pair_of(w0, j + 1), sc[0][c]);
-                    const uint32_t a1 = hmul2(pair_of(w1, j), sc[1][c]), a3 = hmul2(pair_of(w1, j + 1), sc[1][c]);
+                for (int j = 0; j < 2 * NG; ++j) {
+                    const uint4 w = __ldg(src + j);
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int n = 0; n < kNT; ++n)
-                        mma16816(s[a][n], a0, a1, a2, a3, qf[n][4 * c + q][0], qf[n][4 * c + q][1]);
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 v = cache::float2_of_bf16x2(u[e]);
+                        x[8 * j + 2 * e] = v.x;
+                        x[8 * j + 2 * e + 1] = v.y;
+                        peak = fmaxf(peak, fmaxf(fabsf(v.x), fabsf(v.y)));
+                    }
                 }
-        }
-        // masks: the positions of the thread's four keys
-        const bool whole = __all_sync(0xffffffffu, pos0 < see_lo);
-        int kp[2][2];
-        if (!whole) {
+            } else {
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+                for (int j = 0; j < 16 * NG; ++j)
+                    x[j] = 0.0f;
+            }
+            peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
+            peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
+            // exponents of the scale and of its inverse, both normal powers of two
+            const int e = min(max(static_cast<int>(__float_as_uint(peak) >> 23), 1), 253);
+            const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+            const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    kp[a][e] = __shfl_sync(0xffffffffu, pos0, 16 * a + k0 + 2 * e);
-        }
-        bool raise = false;
-        float top[kNT][2];
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
+            for (int s = 0; s < 4 * NG; ++s) {
+                qf[n][s][0] = f16x2_of(x[4 * s] * down, x[4 * s + 1] * down);
+                qf[n][s][1] = f16x2_of(x[4 * s + 2] * down, x[4 * s + 3] * down);
+            }
+            const float fr = up * p.sl2;
+            const int see = r < p.rows && len > 0 ? seen(p, len, i) : 0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float best = -INFINITY;
+                f[n][c] = __shfl_sync(0xffffffffu, fr, 4 * (2 * t + c));
+                lim[n][c] = __shfl_sync(0xffffffffu, see, 4 * (2 * t + c));
+            }
+        }
+
+        float o[MT][kNT][4];
+        float m[kNT][2], l[kNT][2];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    o[j][n][c] = 0.0f;
+        }
+
+        // rows of a tile of 16 keys: K rows k0, k0 + 2 (MMA rows g, g + 8), V rows 4t + (0, 1, 2, 3)
+        // with the pairs swapped for t > 1
+        const int k0 = 4 * (g >> 1) + ((g & 1) ^ (g >> 2));
+        const int v0 = 4 * t + (t >> 1), v1 = 4 * t + 1 - (t >> 1);
+        uint8_t *stage = smem_raw + warp * kStages * Sh::kStage;
+
+        // Bulk: lane 2 a + half < 8 copies array a (K codes, V codes, K scales, V scales) of a half.
+        const int half = lane & 1, array = lane >> 1;
+        const CacheView &view = array & 1 ? p.cv : p.ck;
+        const uint8_t *b_base = array < 2 ? view.data : view.scale;
+        const long long b_page = array < 2 ? view.page_stride : view.scale_stride;
+        const int b_row = array < 2 ? view.row_bytes : view.scale_bytes;
+        const int b_to = (array == 0 ? 0 : array == 1 ? Sh::kV : array == 2 ? Sh::kKs : Sh::kVs) + half * 16 * b_row;
+        constexpr uint32_t kTileBytes = Sh::kStage / 2;
+
+        // Three blocks ahead: the lane's position; the next: its page; two ahead: the
+        // copies.  Nothing that a load brought is looked at before the step that needs it.
+        int pos_f = -1, pos_p = kNoKey, page_p = -1, row_p = 0;
+        auto fetch_pos = [&](int blk) {
+            pos_f = -1;
+            if (blk < b_hi) {
+                const int slot = blk * kBlock + (kBulk ? 16 * half : lane);
+                if (slot < slots)
+                    pos_f = !kBulk && list ? __ldg(list + slot) : slot;
+            }
+        };
+        auto fetch_page = [&]() {
+            const bool in = pos_f >= 0 && pos_f < see_hi;
+            const int n = in ? static_cast<int>(p.pm.div.div(pos_f)) : 0;
+            const bool has = in && n < p.pm.max_pages;
+            page_p = has ? __ldg(table + n) : -1;
+            row_p = gr.h * p.pm.page_size + (has ? pos_f - n * p.pm.page_size : 0);
+            pos_p = has ? pos_f : kNoKey;
+        };
+        // starts a block's copies; returns the lane's position in it (kNoKey: none)
+        auto start = [&](int blk, int at) -> int {
+            int pos = kNoKey;
+            if (blk < b_hi) {
+                const int page = page_p >= 0 && page_p < p.pm.num_pages ? page_p : -1;
+                const uint32_t has = __ballot_sync(0xffffffffu, page >= 0);
+                const uint32_t to = smem_u32(stage + at * Sh::kStage);
+                if constexpr (kBulk) {
+                    const int slot = blk * kBlock + lane;
+                    if (has >> (lane >> 4) & 1u && slot < slots)
+                        pos = slot;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&bars[at], kTileBytes * __popc(has & 3u));
+                    __syncwarp();
+                    if (lane < 8 && page >= 0)
+                        bulk_copy(to + b_to, b_base + page * b_page + static_cast<long long>(row_p) * b_row, 16 * b_row, &bars[at]);
+                } else {
+                    pos = page >= 0 ? pos_p : kNoKey;
+                    stage_codes<kDk, kBlock>(to, data_at(p.ck, page, row_p), has, lane);
+                    stage_codes<kDv, kBlock>(to + Sh::kV, data_at(p.cv, page, row_p), has, lane);
+                    stage_scales<kDk>(to + Sh::kKs, lane, scale_at(p.ck, page, row_p), page >= 0);
+                    stage_scales<kDv>(to + Sh::kVs, lane, scale_at(p.cv, page, row_p), page >= 0);
+                }
+            }
+            if constexpr (!kBulk)
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            return pos;
+        };
+        int blk = b_lo + warp;
+        fetch_pos(blk);
+        fetch_page();
+        fetch_pos(blk + kWarps);
+        int to = at;
+        auto after = [](int s) { return s == kStages - 1 ? 0 : s + 1; };
+        int pos0 = start(blk, to);
+        fetch_page();
+        fetch_pos(blk + 2 * kWarps);
+        to = after(to);
+        int pos1 = start(blk + kWarps, to);
+        fetch_page();
+        fetch_pos(blk + 3 * kWarps);
+        to = after(to);
+        for (; blk < b_hi; blk += kWarps) {
+            if constexpr (kBulk) {
+                const bool landed = wait_bounded(&bars[at], phase, ctl, 30, blk);
+                if (!__all_sync(0xffffffffu, landed))
+                    break;
+                // what lies behind the sequence in its page may be anything, a NaN scale too:
+                // those keys' P is zero, so their V is made zero
+                if (__any_sync(0xffffffffu, pos0 == kNoKey)) {
+                    if (pos0 == kNoKey)
+                        for (int j = 0; j < kDv / 16; j += 4)
+                            *reinterpret_cast<uint32_t *>(stage + at * Sh::kStage + Sh::kVs + lane * (kDv / 16) + j) = 0u;
+                    fence_proxy_async_smem();                      // before the stage's next copies
+                }
+            } else {
+                asm volatile("cp.async.wait_group 1;" ::: "memory");   // this block's have landed
+            }
+            __syncwarp();                                          // every lane's; and the stage before is free
+            const int pos2 = start(blk + 2 * kWarps, to);
+            fetch_page();
+            fetch_pos(blk + 4 * kWarps);
+            const uint8_t *cur = stage + at * Sh::kStage;
+            phase ^= at == kStages - 1;
+            at = after(at);
+            to = after(to);
+            // S^T of two tiles of 16 keys
+            float s[2][kNT][4];
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        s[a][n][c] = 0.0f;
+                // the thread's parts of its two rows
+                uint32_t kw[2][2 * NG], sc[2][NG];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 16 * a + k0 + 2 * e;
+                    read_staged<kDk / 32, 8 * NG, kBulk>(cur, r, 8 * NG * t, kw[e]);
+                    const uint8_t *s8 = cur + Sh::kKs + r * (kDk / 16) + NG * t;
+#pragma unroll
+                    for (int c = 0; c < NG; c += 2) {             // scales, each in both halves
+                        const uint32_t two = cache::f16x2_of_e4m3x2(
+                            NG % 2 == 0 ? *reinterpret_cast<const uint16_t *>(s8 + c) : s8[c] | (c + 1 < NG ? s8[c + 1] << 8 : 0));
+                        sc[e][c] = __byte_perm(two, 0u, 0x1010);
+                        if (c + 1 < NG)
+                            sc[e][c + 1] = __byte_perm(two, 0u, 0x3232);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < NG; ++c)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t w0 = kw[0][2 * c + (q >> 1)], w1 = kw[1][2 * c + (q >> 1)];
+                        const int j = 2 * (q & 1);
+                        const uint32_t a0 = hmul2(pair_of(w0, j), sc[0][c]), a2 = hmul2(pair_of(w0, j + 1), sc[0][c]);
+                        const uint32_t a1 = hmul2(pair_of(w1, j), sc[1][c]), a3 = hmul2(pair_of(w1, j + 1), sc[1][c]);
+#pragma unroll
+                        for (int n = 0; n < kNT; ++n)
+                            mma16816(s[a][n], a0, a1, a2, a3, qf[n][4 * c + q][0], qf[n][4 * c + q][1]);
+                    }
+            }
+            // masks: the positions of the thread's four keys
+            const bool whole = __all_sync(0xffffffffu, pos0 < see_lo);
+            int kp[2][2];
+            if (!whole) {
 #pragma unroll
                 for (int a = 0; a < 2; ++a)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = s[a][n][2 * e + c] * f[n][c];
-                        if (!whole && kp[a][e] >= lim[n][c])
-                            x = -INFINITY;
-                        s[a][n][2 * e + c] = x;
-                        best = fmaxf(best, x);
-                    }
-                top[n][c] = best;
-                raise = raise || best > m[n][c] + kLag;   // (-inf > -inf is false)
+                    for (int e = 0; e < 2; ++e)
+                        kp[a][e] = __shfl_sync(0xffffffffu, pos0, 16 * a + k0 + 2 * e);
             }
-        if (__any_sync(0xffffffffu, raise)) {
+            bool raise = false;
+            float top[kNT][2];
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float best = top[n][c];
+                    float best = -INFINITY;
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1)
-                        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
-                    if (best > m[n][c]) {
-                        const float a = ex2_approx(m[n][c] - best);   // first keys: 2^-inf = 0
-                        m[n][c] = best;
-                        l[n][c] *= a;
+                    for (int a = 0; a < 2; ++a)
 #pragma unroll
-                        for (int j = 0; j < MT; ++j) {
-                            o[j][n][c] *= a;
-                            o[j][n][2 + c] *= a;
+                        for (int e = 0; e < 2; ++e) {
+                            float x = s[a][n][2 * e + c] * f[n][c];
+                            if (!whole && kp[a][e] >= lim[n][c])
+                                x = -INFINITY;
+                            s[a][n][2 * e + c] = x;
+                            best = fmaxf(best, x);
+                        }
+                    top[n][c] = best;
+                    raise = raise || best > m[n][c] + kLag;   // (-inf > -inf is false)
+                }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float best = top[n][c];
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1)
+                            best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
+                        if (best > m[n][c]) {
+                            const float a = ex2_approx(m[n][c] - best);   // first keys: 2^-inf = 0
+                            m[n][c] = best;
+                            l[n][c] *= a;
+#pragma unroll
+                            for (int j = 0; j < MT; ++j) {
+                                o[j][n][c] *= a;
+                                o[j][n][2 + c] *= a;
+                            }
                         }
                     }
-                }
-        }
-        // P, its sums, and P^T as the B operand
-        uint32_t pb[2][kNT][2];
+            }
+            // P, its sums, and P^T as the B operand
+            uint32_t pb[2][kNT][2];
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-            const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0];
-            const float m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+            for (int n = 0; n < kNT; ++n) {
+                const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0];
+                const float m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float p0 = ex2_approx(s[a][n][2 * e] - m0);
+                        const float p1 = ex2_approx(s[a][n][2 * e + 1] - m1);
+                        l[n][0] += p0;
+                        l[n][1] += p1;
+                        pb[a][n][e] = transpose8x8(f16x2_of(p0, p1));
+                    }
+            }
+            // O^T += V^T P^T
 #pragma unroll
             for (int a = 0; a < 2; ++a)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float p0 = ex2_approx(s[a][n][2 * e] - m0);
-                    const float p1 = ex2_approx(s[a][n][2 * e + 1] - m1);
-                    l[n][0] += p0;
-                    l[n][1] += p1;
-                    pb[a][n][e] = transpose8x8(f16x2_of(p0, p1));
+                for (int u = 0; u < NU; ++u) {
+                    uint32_t vw[4][VU / 8], sc[2];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        read_staged<kDv / 32, VU / 2, kBulk>(cur + Sh::kV, 16 * a + ((e & 1) ? v1 : v0) + (e & 2), 4 * VU * u + (VU / 2) * g,
+                                                      vw[e]);
+                    const uint8_t *s8 = cur + Sh::kVs + (VU / 2) * u + (VU * g) / 16;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        sc[e] = cache::f16x2_of_e4m3x2(s8[(16 * a + v0 + 2 * e) * (kDv / 16)] |
+                                                       s8[(16 * a + v1 + 2 * e) * (kDv / 16)] << 8);
+#pragma unroll
+                    for (int w = 0; w < VU / 8; ++w) {
+                        uint32_t lo[2], hi[2];              // even and odd dimensions, a byte = two keys
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t x = vw[2 * e][w], y = vw[2 * e + 1][w];
+                            lo[e] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
+                            hi[e] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a0 = hmul2(pair_of(lo[0], j), sc[0]), a1 = hmul2(pair_of(hi[0], j), sc[0]);
+                            const uint32_t a2 = hmul2(pair_of(lo[1], j), sc[1]), a3 = hmul2(pair_of(hi[1], j), sc[1]);
+#pragma unroll
+                            for (int n = 0; n < kNT; ++n)
+                                mma16816(o[(VU / 2) * u + 4 * w + j][n], a0, a1, a2, a3, pb[a][n][0], pb[a][n][1]);
+                        }
+                    }
                 }
+            pos0 = pos1;
+            pos1 = pos2;
         }
-        // O^T += V^T P^T
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                uint32_t vw[4][VU / 8], sc[2];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    read_staged<kDv / 32, VU / 2>(cur + Sh::kV, 16 * a + ((e & 1) ? v1 : v0) + (e & 2), 4 * VU * u + (VU / 2) * g,
-                                                  vw[e]);
-                const uint8_t *s8 = cur + Sh::kVs + (VU / 2) * u + (VU * g) / 16;
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    sc[e] = cache::f16x2_of_e4m3x2(s8[(16 * a + v0 + 2 * e) * (kDv / 16)] |
-                                                   s8[(16 * a + v1 + 2 * e) * (kDv / 16)] << 8);
-#pragma unroll
-                for (int w = 0; w < VU / 8; ++w) {
-                    uint32_t lo[2], hi[2];              // even and odd dimensions, a byte = two keys
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t x = vw[2 * e][w], y = vw[2 * e + 1][w];
-                        lo[e] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
-                        hi[e] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t a0 = hmul2(pair_of(lo[0], j), sc[0]), a1 = hmul2(pair_of(hi[0], j), sc[0]);
-                        const uint32_t a2 = hmul2(pair_of(lo[1], j), sc[1]), a3 = hmul2(pair_of(hi[1], j), sc[1]);
-#pragma unroll
-                        for (int n = 0; n < kNT; ++n)
-                            mma16816(o[(VU / 2) * u + 4 * w + j][n], a0, a1, a2, a3, pb[a][n][0], pb[a][n][1]);
-                    }
-                }
-            }
-        pos0 = pos1;
-        pos1 = pos2;
-    }
-    cp_async_wait_all();
-    __syncthreads();                                     // the staging becomes the join's buffer
+        // after a wait that ran out: the copies still on their way land before the CTA goes on
+        if (kBulk && blk < b_hi) {
+            wait_drain(&bars[at], phase);
+            if (blk + kWarps < b_hi)
+                wait_drain(&bars[after(at)], phase ^ (at == kStages - 1));
+        }
+        cp_async_wait_all();
+        __syncthreads();                                     // the staging becomes the join's buffer
+        const bool failed = kBulk && *ctl.abort;             // (the same for every warp)
 
-    // join the warps: every warp's O, maxima and sums go to shared memory
-    float *smem = reinterpret_cast<float *>(smem_raw);
-    float *mine = smem + warp * RT * (kDv + 2);
+        // join the warps: every warp's O, maxima and sums go to shared memory
+        float *smem = reinterpret_cast<float *>(smem_raw);
+        float *mine = smem + warp * RT * (kDv + 2);
 #pragma unroll
-    for (int n = 0; n < kNT; ++n)
+        for (int n = 0; n < kNT; ++n)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float sum = l[n][c];
+            for (int c = 0; c < 2; ++c) {
+                float sum = l[n][c];
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            float *row = mine + (8 * n + 2 * t + c) * (kDv + 2);
-            if (g == 0) {
-                row[kDv] = m[n][c];
-                row[kDv + 1] = sum;
+                for (int d = 4; d < 32; d <<= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                float *row = mine + (8 * n + 2 * t + c) * (kDv + 2);
+                if (g == 0) {
+                    row[kDv] = m[n][c];
+                    row[kDv + 1] = sum;
+                }
+                // m-tile j of unit u: rows g, g + 8 are dimensions 8 VU u + VU g + 2j, + 1
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    const int d = 8 * VU * (j / (VU / 2)) + VU * g + 2 * (j % (VU / 2));
+                    *reinterpret_cast<float2 *>(row + d) = make_float2(o[j][n][c], o[j][n][2 + c]);
+                }
             }
-            // m-tile j of unit u: rows g, g + 8 are dimensions 8 VU u + VU g + 2j, + 1
+        __syncthreads();
+        for (int r = warp; r < RT && gr.r0 + r < p.rows; r += kWarps) {
+            const float *row = smem + r * (kDv + 2);
+            float top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const int d = 8 * VU * (j / (VU / 2)) + VU * g + 2 * (j % (VU / 2));
-                *reinterpret_cast<float2 *>(row + d) = make_float2(o[j][n][c], o[j][n][2 + c]);
+            for (int w = 0; w < kWarps; ++w)
+                top = fmaxf(top, row[w * RT * (kDv + 2) + kDv]);
+            float a[kWarps], sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float *wr = row + w * RT * (kDv + 2);
+                a[w] = top == -INFINITY ? 0.0f : ex2_approx(wr[kDv] - top);
+                sum += a[w] * wr[kDv + 1];
             }
-        }
-    __syncthreads();
-    for (int r = warp; r < RT && gr.r0 + r < p.rows; r += kWarps) {
-        const float *row = smem + r * (kDv + 2);
-        float top = -INFINITY;
+            if (hi - lo < all) {
+                // a piece: the CTA's first one ends a tile that another began, or it begins one
+                float *dst = p.part + (static_cast<long long>(2 * blockIdx.x + (lo > 0 ? 0 : 1)) * RT + r) * (kDv + 2);
+                for (int d = lane; d < kDv; d += 32) {
+                    float x = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            top = fmaxf(top, row[w * RT * (kDv + 2) + kDv]);
-        float a[kWarps], sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float *wr = row + w * RT * (kDv + 2);
-            a[w] = top == -INFINITY ? 0.0f : ex2_approx(wr[kDv] - top);
-            sum += a[w] * wr[kDv + 1];
-        }
-        if (p.splits > 1) {
-            float *dst = p.part + (static_cast<long long>(blockIdx.x) * RT + r) * (kDv + 2);
+                    for (int w = 0; w < kWarps; ++w)
+                        x += a[w] * row[w * RT * (kDv + 2) + d];
+                    dst[d] = x;
+                }
+                if (lane == 0) {
+                    dst[kDv] = top;
+                    dst[kDv + 1] = sum;
+                }
+                continue;
+            }
+            int i, head;
+            row_of(p, gr, gr.r0 + r, i, head);
+            const long long out_row = (static_cast<long long>(gr.b) * p.S + i) * p.HA + head;
+            const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
             for (int d = lane; d < kDv; d += 32) {
                 float x = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
                     x += a[w] * row[w * RT * (kDv + 2) + d];
-                dst[d] = x;
+                p.out[out_row * kDv + d] = __float2bfloat16_rn(x * inv);
             }
-            if (lane == 0) {
-                dst[kDv] = top;
-                dst[kDv + 1] = sum;
-            }
-            continue;
+            if (p.lse && lane == 0)
+                p.lse[out_row] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
         }
-        int i, head;
-        row_of(p, gr, gr.r0 + r, i, head);
-        const long long at = (static_cast<long long>(gr.b) * p.S + i) * p.HA + head;
-        const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
-        for (int d = lane; d < kDv; d += 32) {
-            float x = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                x += a[w] * row[w * RT * (kDv + 2) + d];
-            p.out[at * kDv + d] = __float2bfloat16_rn(x * inv);
-        }
-        if (p.lse && lane == 0)
-            p.lse[at] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        fence_proxy_async_smem();                            // before the next segment's bulk copies
+        __syncthreads();
+        if (failed)
+            break;
     }
 }
 
-// Joins the shares of one row: out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
-// One warp a row.
+// Joins the pieces of the row tiles that several CTAs of the kernel above share: out =
+// sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.  A block takes rows of sequence
+// blockIdx.x, its warps every fourth piece of a row.
+__global__ void __launch_bounds__(kThreads) cache_attn_pieces_kernel(const AttnParams p, int Dv, int tile_rows)
+{
+    __shared__ long long scratch[kWarps];
+    __shared__ float part[kWarps][256 + 2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.x;
+    const int all = chunks_of(p, b);
+    if (all == 0)
+        return;                                          // written by the kernel above
+    const long long total = chunks_before(p, p.B, scratch), first = chunks_before(p, b, scratch);
+    const int ctas = static_cast<int>(min(static_cast<long long>(p.ctas), total));
+    for (int row = blockIdx.y; row < p.S * p.HA; row += gridDim.y) {
+        const int i = row / p.HA, head = row - i * p.HA, h = head / p.G;
+        const int r = p.idx ? head - h * p.G : i * p.G + head - h * p.G;
+        const int w = ((p.idx ? i * p.H : 0) + h) * p.tiles + r / tile_rows;
+        const long long start = first + static_cast<long long>(w) * all;
+        const int k0 = cta_of(start, total, ctas), k1 = cta_of(start + all - 1, total, ctas);
+        if (k0 == k1)
+            continue;                                    // one CTA had the whole tile
+        const long long stride = static_cast<long long>(tile_rows) * (Dv + 2);
+        // the first CTA's piece begins the tile (its second slot), the others' end or fill it
+        auto piece = [&](int k) {
+            return p.part + (2ll * k + (k == k0 ? 1 : 0)) * stride + (r % tile_rows) * (Dv + 2);
+        };
+        float top = -INFINITY;
+        for (int k = k0 + threadIdx.x; k <= k1; k += kThreads)
+            top = fmaxf(top, piece(k)[Dv]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        __syncthreads();                                 // (the row before has been read)
+        if (lane == 0)
+            part[warp][256] = top;
+        __syncthreads();
+        top = fmaxf(fmaxf(part[0][256], part[1][256]), fmaxf(part[2][256], part[3][256]));
+        const float base = top == -INFINITY ? 0.0f : top;
+        float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
+#pragma unroll 4
+        for (int k = k0 + warp; k <= k1; k += kWarps) {
+            const float *src = piece(k);
+            const float a = ex2_approx(src[Dv] - base);
+            sum += a * src[Dv + 1];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (64 * j < Dv) {
+                    const float2 v = *reinterpret_cast<const float2 *>(src + 64 * j + 2 * lane);
+                    x[2 * j] += a * v.x;
+                    x[2 * j + 1] += a * v.y;
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (64 * j < Dv)
+                *reinterpret_cast<float2 *>(&part[warp][64 * j + 2 * lane]) = make_float2(x[2 * j], x[2 * j + 1]);
+        if (lane == 0)
+            part[warp][257] = sum;
+        __syncthreads();
+        sum = part[0][257] + part[1][257] + part[2][257] + part[3][257];
+        const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
+        const long long out_row = static_cast<long long>(b) * p.S * p.HA + row;
+        for (int d = 2 * threadIdx.x; d < Dv; d += 2 * kThreads) {
+            const float u = part[0][d] + part[1][d] + part[2][d] + part[3][d];
+            const float v = part[0][d + 1] + part[1][d + 1] + part[2][d + 1] + part[3][d + 1];
+            *reinterpret_cast<uint32_t *>(p.out + out_row * Dv + d) = cache::bf16x2_of(u * inv, v * inv);
+        }
+        if (p.lse && threadIdx.x == 0)
+            p.lse[out_row] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
+// Joins the wide kernel's shares of one row, one warp a row.
 __global__ void __launch_bounds__(128) cache_attn_join_kernel(const AttnParams p, int Dv, int tile_rows,
                                                               long long rows)
 {

@@ -242,15 +242,15 @@ __device__ void wide_gather(const WideParams &wp, uint8_t *smem, WideBarriers *b
                     mask[gw] = static_cast<uint8_t>(bits);
             }
             const uint32_t to = smem_u32(raw + (g & 1) * Sh::kRaw);
-            stage_codes<kDk, kRows>(p.ck, to, page, row2, lane);
-            stage_codes<kDv, kRows>(p.cv, to + Sh::kRawV, page, row2, lane);
+            stage_codes<kDk, kRows>(to, data_at(p.ck, page, row2), bits, lane);
+            stage_codes<kDv, kRows>(to + Sh::kRawV, data_at(p.cv, page, row2), bits, lane);
             // scales: the keys' by lanes 0.., the values' by lanes 16..
             const int pg = __shfl_sync(0xffffffffu, page, lane & 15), ro = __shfl_sync(0xffffffffu, row2, lane & 15);
             if ((lane & 15) < kRows) {
                 if (lane < 16)
-                    stage_scales<kDk>(p.ck, to + Sh::kRawKs, lane, pg, ro);
+                    stage_scales<kDk>(to + Sh::kRawKs, lane, scale_at(p.ck, pg, ro), pg >= 0);
                 else
-                    stage_scales<kDv>(p.cv, to + Sh::kRawVs, lane - 16, pg, ro);
+                    stage_scales<kDv>(to + Sh::kRawVs, lane - 16, scale_at(p.cv, pg, ro), pg >= 0);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");

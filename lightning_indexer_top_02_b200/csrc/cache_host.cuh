@@ -407,10 +407,12 @@ using CattnWideFn = void (*)(const csa::cattn::WideParams);
 
 struct CattnPlan {
     bool wide;
+    bool bulk;              // tiles of 16 keys lie together in a page (the register kernel)
     int keys, raw;          // of the wide kernel: keys of a tile, staging bytes
     int tile_rows, tiles, rows, splits;
     long long works;
     size_t workspace;
+    int ctas;               // of the register kernel: those that share the chunks, 0: one a row tile
     CattnFn fn;
     CattnWideFn wide_fn;
     int smem;
@@ -426,11 +428,13 @@ void cattn_pick(CattnPlan *pl)
         pl->wide_fn = pl->tile_rows == kWideRows ? cache_attn_wide_kernel<kDk, kDv, false>
                                                  : cache_attn_wide_kernel<kDk, kDv, true>;
     } else if (pl->tile_rows == 8) {
-        pl->fn = cache_attn_kernel<kDk, kDv, 1>;
+        pl->fn = pl->bulk ? cache_attn_kernel<kDk, kDv, 1, true> : cache_attn_kernel<kDk, kDv, 1, false>;
         pl->smem = Shape<kDk, kDv, 1>::kSmem;
+        pl->ctas = Shape<kDk, kDv, 1>::kCtas;
     } else {
-        pl->fn = cache_attn_kernel<kDk, kDv, 2>;
+        pl->fn = pl->bulk ? cache_attn_kernel<kDk, kDv, 2, true> : cache_attn_kernel<kDk, kDv, 2, false>;
         pl->smem = Shape<kDk, kDv, 2>::kSmem;
+        pl->ctas = Shape<kDk, kDv, 2>::kCtas;
     }
 }
 
@@ -483,6 +487,8 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
     const int H = a->cache_k.H, G = a->HA / H;
     pl->rows = a->idx ? G : a->S * G;
     pl->wide = pl->rows > 16;
+    const CacheView ck = cache_view(a->cache_k), cv = cache_view(a->cache_v);
+    pl->bulk = !a->idx && a->cache_k.page_size % 16 == 0 && ck.scale_stride % 16 == 0 && cv.scale_stride % 16 == 0;
     pl->tile_rows = pl->rows <= 8 ? 8 : pl->rows <= 16 ? 16 : pl->rows <= 64 ? 64 : csa::cattn::kWideRows;
     pl->tiles = (pl->rows + pl->tile_rows - 1) / pl->tile_rows;
     pl->works = static_cast<long long>(a->B) * (a->idx ? a->S : 1) * H * pl->tiles;
@@ -510,19 +516,17 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
             }
         }
     } else {
-        // the keys are shared out until the GPU is full twice over, but a share is
-        // at least one block of 32 keys a warp
-        const long long per = csa::cattn::kBlock * csa::cattn::kWarps;
-        splits = (6ll * sms + pl->works - 1) / pl->works;
-        if (splits > (most + per - 1) / per)
-            splits = (most + per - 1) / per;
+        // as many CTAs as the GPU holds share the chunks; where no tile has more
+        // than one chunk, a CTA each, and nothing to join
+        const long long chunks = (most + csa::cattn::kChunk - 1) / csa::cattn::kChunk;
+        const long long held = static_cast<long long>(sms) * pl->ctas;
+        pl->ctas = chunks <= 1 ? 0 : static_cast<int>(pl->works * chunks < held ? pl->works * chunks : held);
     }
     pl->splits = static_cast<int>(splits < 1 ? 1 : splits > 256 ? 256 : splits);
     if (pl->works * pl->splits >= kIntLimit)
         return CSA_ERR_UNSUPPORTED;
-    pl->workspace = pl->splits > 1 ? static_cast<size_t>(pl->works) * pl->splits * pl->tile_rows *
-                                         (a->cache_v.D + 2) * sizeof(float)
-                                   : 0;
+    const long long pieces = pl->wide ? (pl->splits > 1 ? pl->works * pl->splits : 0) : 2ll * pl->ctas;
+    pl->workspace = static_cast<size_t>(pieces) * pl->tile_rows * (a->cache_v.D + 2) * sizeof(float);
     return CSA_OK;
 }
 
@@ -626,7 +630,10 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     p.v_scale = a->cache_v.tensor_scale;
     p.out = static_cast<__nv_bfloat16 *>(a->out);
     p.lse = a->lse;
+    p.wait_limit = static_cast<long long>(g_wait_limit);
     p.splits = pl.splits;
+    p.ctas = pl.ctas;
+    p.works = static_cast<int>(pl.works / a->B);
     p.tiles = pl.tiles;
     p.rows = pl.rows;
     p.capacity = a->max_pages * a->cache_k.page_size;
@@ -643,15 +650,24 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     } else if (cudaFuncSetAttribute(pl.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem) != cudaSuccess) {
         st = CSA_ERR_CUDA;
     } else {
-        pl.fn<<<static_cast<unsigned>(pl.works * pl.splits), csa::cattn::kThreads, pl.smem, stream>>>(p);
+        pl.fn<<<static_cast<unsigned>(pl.ctas ? pl.ctas : pl.works), csa::cattn::kThreads, pl.smem, stream>>>(p);
         st = launched();
     }
     if (st == CSA_OK && !mark(1, stream))
         st = CSA_ERR_CUDA;
-    if (st == CSA_OK && pl.splits > 1) {
-        const long long rows = static_cast<long long>(a->B) * a->S * a->HA;
-        csa::cattn::cache_attn_join_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(
-            p, a->cache_v.D, pl.tile_rows, rows);
+    const long long rows = static_cast<long long>(a->B) * a->S * a->HA;
+    const bool join = pl.wide ? pl.splits > 1 : pl.ctas > 0;
+    if (st == CSA_OK && join) {
+        if (pl.wide) {
+            csa::cattn::cache_attn_join_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(
+                p, a->cache_v.D, pl.tile_rows, rows);
+        } else {
+            // a block for every row, or several rows a block when there are many
+            const int per = a->S * a->HA, most = 32 * device_sms() / a->B;
+            const dim3 grid(a->B, per < most ? per : most < 1 ? 1 : most);
+            csa::cattn::cache_attn_pieces_kernel<<<grid, csa::cattn::kThreads, 0, stream>>>(p, a->cache_v.D,
+                                                                                           pl.tile_rows);
+        }
         st = launched();
         if (st == CSA_OK && !mark(2, stream))
             st = CSA_ERR_CUDA;
