@@ -8,7 +8,7 @@
 //   O^T [16 dims x 8 rows] += V^T [16 x 16 keys] . P^T [16 keys x 8]
 // With at most 16 rows the work is bound by reading the cache (9/16 byte an
 // element against 4 rows' flops an element), so what matters is how few
-// instructions stand between a code and its use.  A warp takes blocks of 32 keys;
+// instructions stand between a code and its use.  A warp takes blocks of 64 (32) keys;
 // their codes and scales come by cp.async two blocks ahead into the warp's own
 // staging rows and go from there into registers in the layout of the MMA's A
 // operand: no transposition, and no barrier between warps.
@@ -40,10 +40,10 @@
 // copy each; else every row is found by itself and copied 16 bytes at a time, which
 // takes about 150 instructions more of some 750 a block.
 //
-// The CTAs that the GPU holds share out all the chunks of 128 keys of all row tiles,
+// The CTAs that the GPU holds share out all the chunks (256 or 128 keys) of all row tiles,
 // evenly and in order, whatever the sequences' lengths: a CTA's share is a run of
 // chunks, which ends one tile, takes whole ones and begins another.  In a tile the
-// warps take blocks of 32 keys in turn and keep their own running maxima, sums and O,
+// warps take blocks of keys in turn and keep their own running maxima, sums and O,
 // which are joined in shared memory; the pieces of a tile that several CTAs share
 // are joined by a second kernel.
 #pragma once
@@ -59,9 +59,6 @@ using cache::PageMap;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kBlock = 32;                  // keys a warp takes at a time
-constexpr int kChunk = kBlock * kWarps;     // keys that are shared out together
-constexpr int kStages = 3;                  // blocks staged: one in use, two on their way
 constexpr float kLag = 8.0f;                // the maximum is raised past 2^8 only
 constexpr int kNoKey = 0x7FFFFFFF;          // a position no query sees
 
@@ -82,6 +79,7 @@ struct AttnParams {
     int splits;                             // wide kernel: shares of the keys
     int ctas;                               // CTAs that share the chunks; 0: one a row tile (at most a chunk each)
     int works;                              // row tiles of a sequence
+    int chunk;                              // keys that are shared out together
     int tiles;                              // row tiles of a group
     int rows;                               // query rows of a group: S * G, or G with idx
     int capacity;                           // positions the page table reaches
@@ -283,6 +281,12 @@ struct Shape {
     static constexpr int NU = kDv / (8 * VU);            // and how many times
     static constexpr int MT = kDv / 16;                  // output m-tiles
     static constexpr int kRows = 8 * kNT;
+    // keys a warp takes at a time: what a block costs beside its keys (finding, copying
+    // and waiting, about 170 instructions) is spread over 64 where shared memory allows
+    static constexpr int kBlock = kDk + kDv <= 256 ? 64 : 32;
+    static constexpr int kTiles = kBlock / 16, kSets = kBlock / 32;      // MMA tiles; keys a lane looks up
+    static constexpr int kStages = kBlock == 64 ? 2 : 3;                 // blocks in use and on their way
+    static constexpr int kChunk = kBlock * kWarps;                       // keys that are shared out together
     // staging of a block: K codes, V codes, K scales, V scales
     static constexpr int kV = kBlock * kDk / 2, kKs = kV + kBlock * kDv / 2;
     static constexpr int kVs = kKs + kBlock * kDk / 16, kStage = kVs + kBlock * kDv / 16;
@@ -291,7 +295,7 @@ struct Shape {
     static constexpr int kBars = kJoin > kStaging ? kJoin : kStaging;    // barriers, abort flag
     static constexpr int kSmem = kBars + kWarps * kStages * 8 + 16;
     // blocks an SM holds: registers for O and the query, shared memory for the staging
-    static constexpr int kCtas = kDk + kDv <= 256 && kNT == 1 ? 4 : kDk + kDv <= 256 ? 3 : kDk + kDv <= 384 && kNT == 1 ? 3 : 2;
+    static constexpr int kCtas = kNT == 1 && kDk + kDv <= 384 ? 3 : 2;
 };
 
 // Chunks of one row tile of sequence b.  (A tile of early queries sees less of the
@@ -300,7 +304,7 @@ __device__ __forceinline__ int chunks_of(const AttnParams &p, int b)
 {
     const int len = __ldg(p.kv_len + b);
     const int n = len > 0 ? (p.idx ? p.topk : min(len, p.capacity)) : 0;
-    return static_cast<int>((static_cast<unsigned>(n) + kChunk - 1) / kChunk);
+    return static_cast<int>((static_cast<unsigned>(n) + p.chunk - 1) / p.chunk);   // (a power of two)
 }
 
 // Sum over the block's kThreads threads (scratch: kWarps words).
@@ -374,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
 {
     using Sh = Shape<kDk, kDv, kNT>;
     constexpr int NG = Sh::NG, VU = Sh::VU, NU = Sh::NU, MT = Sh::MT, RT = Sh::kRows;
+    constexpr int kBlock = Sh::kBlock, kTiles = Sh::kTiles, kSets = Sh::kSets, kStages = Sh::kStages;
     extern __shared__ __align__(16) uint8_t smem_raw[];  // staging, then [warp][row][Dv + 2]
     __shared__ long long scratch[kWarps];
     __shared__ Found found;
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
         const int see_lo = len > 0 ? seen(p, len, gr.i0 + static_cast<int>(p.div_G.div(gr.r0))) : 0;
         const int slots = p.idx ? (see_hi > 0 ? p.topk : 0) : min(max(see_hi, 0), p.capacity);
         const int blocks = (slots + kBlock - 1) / kBlock;
-        const int b_lo = lo * (kChunk / kBlock), b_hi = min(hi * (kChunk / kBlock), blocks);
+        const int b_lo = lo * kWarps, b_hi = min(hi * kWarps, blocks);
 
         // query fragments: row g of each n-tile, elements 16 NG t.., scaled by a power of two
         uint32_t qf[kNT][4 * NG][2];
@@ -484,14 +489,16 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
             peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
             // exponents of the scale and of its inverse, both normal powers of two
             const int e = min(max(static_cast<int>(__float_as_uint(peak) >> 23), 1), 253);
-            const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+            const float down = __uint_as_float((static_cast<uint32_t>(254 - e) << 23) | (p.sl2 < 0.0f ? 0x80000000u : 0u));
             const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
 #pragma unroll
             for (int s = 0; s < 4 * NG; ++s) {
                 qf[n][s][0] = f16x2_of(x[4 * s] * down, x[4 * s + 1] * down);
                 qf[n][s][1] = f16x2_of(x[4 * s + 2] * down, x[4 * s + 3] * down);
             }
-            const float fr = up * p.sl2;
+            // the scale's sign goes with the query, and the factor is not zero, so that a masked
+        // score times it is -inf
+        const float fr = fmaxf(up * fabsf(p.sl2), 1.17549435e-38f);
             const int see = r < p.rows && len > 0 ? seen(p, len, i) : 0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -519,147 +526,189 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
         const int v0 = 4 * t + (t >> 1), v1 = 4 * t + 1 - (t >> 1);
         uint8_t *stage = smem_raw + warp * kStages * Sh::kStage;
 
-        // Bulk: lane 2 a + half < 8 copies array a (K codes, V codes, K scales, V scales) of a half.
-        const int half = lane & 1, array = lane >> 1;
+        // Bulk: lane kTiles * a + i copies array a (K codes, V codes, K scales, V scales) of tile i.
+        const int tile = lane % kTiles, array = lane / kTiles;
         const CacheView &view = array & 1 ? p.cv : p.ck;
-        const uint8_t *b_base = array < 2 ? view.data : view.scale;
-        const long long b_page = array < 2 ? view.page_stride : view.scale_stride;
         const int b_row = array < 2 ? view.row_bytes : view.scale_bytes;
-        const int b_to = (array == 0 ? 0 : array == 1 ? Sh::kV : array == 2 ? Sh::kKs : Sh::kVs) + half * 16 * b_row;
-        constexpr uint32_t kTileBytes = Sh::kStage / 2;
+        const long long b_page = array < 2 ? view.page_stride : view.scale_stride;
+        const uint8_t *b_base = (array < 2 ? view.data : view.scale) + static_cast<long long>(gr.h) * p.pm.page_size * b_row;
+        const int b_to = (array == 0 ? 0 : array == 1 ? Sh::kV : array == 2 ? Sh::kKs : Sh::kVs) + tile * 16 * b_row;
 
-        // Three blocks ahead: the lane's position; the next: its page; two ahead: the
-        // copies.  Nothing that a load brought is looked at before the step that needs it.
-        int pos_f = -1, pos_p = kNoKey, page_p = -1, row_p = 0;
+        // A lane's keys of a block (bulk: its tile), found ahead of the copies: first the
+        // position, then its page.  Nothing that a load brought is looked at before the
+        // step that needs it.
+        constexpr int kLook = kBulk ? 1 : kSets;
+        int pos_f[kLook], pos_p[kLook], page_p[kLook], off_p[kLook];
         auto fetch_pos = [&](int blk) {
-            pos_f = -1;
-            if (blk < b_hi) {
-                const int slot = blk * kBlock + (kBulk ? 16 * half : lane);
-                if (slot < slots)
-                    pos_f = !kBulk && list ? __ldg(list + slot) : slot;
+#pragma unroll
+            for (int i = 0; i < kLook; ++i) {
+                pos_f[i] = -1;
+                if (blk < b_hi) {
+                    const int slot = blk * kBlock + (kBulk ? 16 * tile : 32 * i + lane);
+                    if (slot < slots)
+                        pos_f[i] = !kBulk && list ? __ldg(list + slot) : slot;
+                }
             }
         };
         auto fetch_page = [&]() {
-            const bool in = pos_f >= 0 && pos_f < see_hi;
-            const int n = in ? static_cast<int>(p.pm.div.div(pos_f)) : 0;
-            const bool has = in && n < p.pm.max_pages;
-            page_p = has ? __ldg(table + n) : -1;
-            row_p = gr.h * p.pm.page_size + (has ? pos_f - n * p.pm.page_size : 0);
-            pos_p = has ? pos_f : kNoKey;
+#pragma unroll
+            for (int i = 0; i < kLook; ++i) {
+                const bool in = pos_f[i] >= 0 && pos_f[i] < see_hi;
+                const int n = in ? static_cast<int>(p.pm.div.div(pos_f[i])) : 0;
+                const bool has = in && n < p.pm.max_pages;
+                page_p[i] = has ? __ldg(table + n) : -1;
+                off_p[i] = has ? pos_f[i] - n * p.pm.page_size : 0;
+                pos_p[i] = pos_f[i];
+            }
         };
-        // starts a block's copies; returns the lane's position in it (kNoKey: none)
-        auto start = [&](int blk, int at) -> int {
-            int pos = kNoKey;
+        // starts a block's copies; pos: the lane's positions in it (kNoKey: none)
+        auto start = [&](int blk, int at, int (&pos)[kSets]) {
+#pragma unroll
+            for (int i = 0; i < kSets; ++i)
+                pos[i] = kNoKey;
             if (blk < b_hi) {
-                const int page = page_p >= 0 && page_p < p.pm.num_pages ? page_p : -1;
-                const uint32_t has = __ballot_sync(0xffffffffu, page >= 0);
                 const uint32_t to = smem_u32(stage + at * Sh::kStage);
                 if constexpr (kBulk) {
-                    const int slot = blk * kBlock + lane;
-                    if (has >> (lane >> 4) & 1u && slot < slots)
-                        pos = slot;
+                    const bool ok = page_p[0] >= 0 && page_p[0] < p.pm.num_pages;
+                    const uint32_t has = __ballot_sync(0xffffffffu, ok) & ((1u << kTiles) - 1u);
+#pragma unroll
+                    for (int i = 0; i < kSets; ++i) {
+                        const int slot = blk * kBlock + 32 * i + lane;
+                        if (has >> (2 * i + (lane >> 4)) & 1u && slot < slots)
+                            pos[i] = slot;
+                    }
                     if (lane == 0)
-                        mbar_arrive_expect_tx(&bars[at], kTileBytes * __popc(has & 3u));
+                        mbar_arrive_expect_tx(&bars[at], Sh::kStage / kTiles * __popc(has));
                     __syncwarp();
-                    if (lane < 8 && page >= 0)
-                        bulk_copy(to + b_to, b_base + page * b_page + static_cast<long long>(row_p) * b_row, 16 * b_row, &bars[at]);
+                    if (lane < 4 * kTiles && ok)
+                        bulk_copy(to + b_to, b_base + page_p[0] * b_page + static_cast<long long>(off_p[0]) * b_row,
+                                  16 * b_row, &bars[at]);
                 } else {
-                    pos = page >= 0 ? pos_p : kNoKey;
-                    stage_codes<kDk, kBlock>(to, data_at(p.ck, page, row_p), has, lane);
-                    stage_codes<kDv, kBlock>(to + Sh::kV, data_at(p.cv, page, row_p), has, lane);
-                    stage_scales<kDk>(to + Sh::kKs, lane, scale_at(p.ck, page, row_p), page >= 0);
-                    stage_scales<kDv>(to + Sh::kVs, lane, scale_at(p.cv, page, row_p), page >= 0);
+#pragma unroll
+                    for (int i = 0; i < kSets; ++i) {
+                        const int page = page_p[i] >= 0 && page_p[i] < p.pm.num_pages ? page_p[i] : -1;
+                        const int row = gr.h * p.pm.page_size + off_p[i];
+                        const uint32_t has = __ballot_sync(0xffffffffu, page >= 0);
+                        pos[i] = page >= 0 ? pos_p[i] : kNoKey;
+                        stage_codes<kDk, 32>(to + 16 * i * kDk, data_at(p.ck, page, row), has, lane);
+                        stage_codes<kDv, 32>(to + Sh::kV + 16 * i * kDv, data_at(p.cv, page, row), has, lane);
+                        stage_scales<kDk>(to + Sh::kKs + 2 * i * kDk, lane, scale_at(p.ck, page, row), page >= 0);
+                        stage_scales<kDv>(to + Sh::kVs + 2 * i * kDv, lane, scale_at(p.cv, page, row), page >= 0);
+                    }
                 }
             }
             if constexpr (!kBulk)
                 asm volatile("cp.async.commit_group;" ::: "memory");
-            return pos;
         };
-        int blk = b_lo + warp;
+        auto after = [](int s) { return s == kStages - 1 ? 0 : s + 1; };
+        // all but one stage are filled before the first block, one block behind another
+        int blk = b_lo + warp, pos[kStages][kSets], to = at;
         fetch_pos(blk);
         fetch_page();
         fetch_pos(blk + kWarps);
-        int to = at;
-        auto after = [](int s) { return s == kStages - 1 ? 0 : s + 1; };
-        int pos0 = start(blk, to);
-        fetch_page();
-        fetch_pos(blk + 2 * kWarps);
-        to = after(to);
-        int pos1 = start(blk + kWarps, to);
-        fetch_page();
-        fetch_pos(blk + 3 * kWarps);
-        to = after(to);
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            start(blk + i * kWarps, to, pos[i]);
+            fetch_page();
+            fetch_pos(blk + (i + 2) * kWarps);
+            to = after(to);
+        }
         for (; blk < b_hi; blk += kWarps) {
+            // the stage that the block before has left takes the next copies
+            start(blk + (kStages - 1) * kWarps, to, pos[kStages - 1]);
+            fetch_page();
+            fetch_pos(blk + (kStages + 1) * kWarps);
             if constexpr (kBulk) {
                 const bool landed = wait_bounded(&bars[at], phase, ctl, 30, blk);
                 if (!__all_sync(0xffffffffu, landed))
                     break;
                 // what lies behind the sequence in its page may be anything, a NaN scale too:
                 // those keys' P is zero, so their V is made zero
-                if (__any_sync(0xffffffffu, pos0 == kNoKey)) {
-                    if (pos0 == kNoKey)
-                        for (int j = 0; j < kDv / 16; j += 4)
-                            *reinterpret_cast<uint32_t *>(stage + at * Sh::kStage + Sh::kVs + lane * (kDv / 16) + j) = 0u;
+                bool all_there = true;
+#pragma unroll
+                for (int i = 0; i < kSets; ++i)
+                    all_there = all_there && pos[0][i] != kNoKey;
+                if (!__all_sync(0xffffffffu, all_there)) {
+#pragma unroll
+                    for (int i = 0; i < kSets; ++i)
+                        if (pos[0][i] == kNoKey)
+                            for (int j = 0; j < kDv / 16; j += 4)
+                                *reinterpret_cast<uint32_t *>(stage + at * Sh::kStage + Sh::kVs +
+                                                              (32 * i + lane) * (kDv / 16) + j) = 0u;
                     fence_proxy_async_smem();                      // before the stage's next copies
+                    __syncwarp();
                 }
             } else {
-                asm volatile("cp.async.wait_group 1;" ::: "memory");   // this block's have landed
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");   // this block's have landed
+                __syncwarp();                                      // every lane's
             }
-            __syncwarp();                                          // every lane's; and the stage before is free
-            const int pos2 = start(blk + 2 * kWarps, to);
-            fetch_page();
-            fetch_pos(blk + 4 * kWarps);
             const uint8_t *cur = stage + at * Sh::kStage;
             phase ^= at == kStages - 1;
             at = after(at);
             to = after(to);
-            // S^T of two tiles of 16 keys
-            float s[2][kNT][4];
+            // S^T of the tiles of 16 keys, two at a time: their MMAs' chains of sums alternate
+            float s[kTiles][kNT][4];
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
+            for (int a0 = 0; a0 < kTiles; a0 += 2) {
+                uint32_t kw[2][2][2 * NG], sc[2][2][NG];      // [tile][row]: the thread's parts of its rows
 #pragma unroll
-                for (int n = 0; n < kNT; ++n)
+                for (int a = 0; a < 2; ++a) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        s[a][n][c] = 0.0f;
-                // the thread's parts of its two rows
-                uint32_t kw[2][2 * NG], sc[2][NG];
+                    for (int n = 0; n < kNT; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = 16 * a + k0 + 2 * e;
-                    read_staged<kDk / 32, 8 * NG, kBulk>(cur, r, 8 * NG * t, kw[e]);
-                    const uint8_t *s8 = cur + Sh::kKs + r * (kDk / 16) + NG * t;
+                        for (int c = 0; c < 4; ++c)
+                            s[a0 + a][n][c] = 0.0f;
 #pragma unroll
-                    for (int c = 0; c < NG; c += 2) {             // scales, each in both halves
-                        const uint32_t two = cache::f16x2_of_e4m3x2(
-                            NG % 2 == 0 ? *reinterpret_cast<const uint16_t *>(s8 + c) : s8[c] | (c + 1 < NG ? s8[c + 1] << 8 : 0));
-                        sc[e][c] = __byte_perm(two, 0u, 0x1010);
-                        if (c + 1 < NG)
-                            sc[e][c + 1] = __byte_perm(two, 0u, 0x3232);
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = 16 * (a0 + a) + k0 + 2 * e;
+                        read_staged<kDk / 32, 8 * NG, kBulk>(cur, r, 8 * NG * t, kw[a][e]);
+                        const uint8_t *s8 = cur + Sh::kKs + r * (kDk / 16) + NG * t;
+#pragma unroll
+                        for (int c = 0; c < NG; c += 2) {     // scales, each in both halves
+                            const uint32_t two = cache::f16x2_of_e4m3x2(
+                                NG % 2 == 0 ? *reinterpret_cast<const uint16_t *>(s8 + c)
+                                            : s8[c] | (c + 1 < NG ? s8[c + 1] << 8 : 0));
+                            sc[a][e][c] = __byte_perm(two, 0u, 0x1010);
+                            if (c + 1 < NG)
+                                sc[a][e][c + 1] = __byte_perm(two, 0u, 0x3232);
+                        }
                     }
                 }
 #pragma unroll
                 for (int c = 0; c < NG; ++c)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t w0 = kw[0][2 * c + (q >> 1)], w1 = kw[1][2 * c + (q >> 1)];
-                        const int j = 2 * (q & 1);
-                        const uint32_t a0 = hmul2(pair_of(w0, j), sc[0][c]), a2 = hmul2(pair_of(w0, j + 1), sc[0][c]);
-                        const uint32_t a1 = hmul2(pair_of(w1, j), sc[1][c]), a3 = hmul2(pair_of(w1, j + 1), sc[1][c]);
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) {
+                            const uint32_t w0 = kw[a][0][2 * c + (q >> 1)], w1 = kw[a][1][2 * c + (q >> 1)];
+                            const int j = 2 * (q & 1);
+                            const uint32_t x0 = hmul2(pair_of(w0, j), sc[a][0][c]);
+                            const uint32_t x1 = hmul2(pair_of(w1, j), sc[a][1][c]);
+                            const uint32_t x2 = hmul2(pair_of(w0, j + 1), sc[a][0][c]);
+                            const uint32_t x3 = hmul2(pair_of(w1, j + 1), sc[a][1][c]);
+#pragma unroll
+                            for (int n = 0; n < kNT; ++n)
+                                mma16816(s[a0 + a][n], x0, x1, x2, x3, qf[n][4 * c + q][0], qf[n][4 * c + q][1]);
+                        }
+            }
+            // masks: the positions of the thread's keys
+            bool seen_all = true;
+#pragma unroll
+            for (int i = 0; i < kSets; ++i)
+                seen_all = seen_all && pos[0][i] < see_lo;
+            if (!__all_sync(0xffffffffu, seen_all)) {
+#pragma unroll
+                for (int a = 0; a < kTiles; ++a)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int at_key = __shfl_sync(0xffffffffu, pos[0][a >> 1], 16 * (a & 1) + k0 + 2 * e);
 #pragma unroll
                         for (int n = 0; n < kNT; ++n)
-                            mma16816(s[a][n], a0, a1, a2, a3, qf[n][4 * c + q][0], qf[n][4 * c + q][1]);
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                if (at_key >= lim[n][c])
+                                    s[a][n][2 * e + c] = -INFINITY;
                     }
-            }
-            // masks: the positions of the thread's four keys
-            const bool whole = __all_sync(0xffffffffu, pos0 < see_lo);
-            int kp[2][2];
-            if (!whole) {
-#pragma unroll
-                for (int a = 0; a < 2; ++a)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        kp[a][e] = __shfl_sync(0xffffffffu, pos0, 16 * a + k0 + 2 * e);
             }
             bool raise = false;
             float top[kNT][2];
@@ -669,17 +718,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
                 for (int c = 0; c < 2; ++c) {
                     float best = -INFINITY;
 #pragma unroll
-                    for (int a = 0; a < 2; ++a)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float x = s[a][n][2 * e + c] * f[n][c];
-                            if (!whole && kp[a][e] >= lim[n][c])
-                                x = -INFINITY;
-                            s[a][n][2 * e + c] = x;
-                            best = fmaxf(best, x);
-                        }
-                    top[n][c] = best;
-                    raise = raise || best > m[n][c] + kLag;   // (-inf > -inf is false)
+                    for (int a = 0; a < kTiles; ++a)
+                        best = fmaxf(best, fmaxf(s[a][n][c], s[a][n][2 + c]));
+                    top[n][c] = best * f[n][c];
+                    raise = raise || top[n][c] > m[n][c] + kLag;   // (-inf > -inf is false)
                 }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -703,17 +745,18 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
                     }
             }
             // P, its sums, and P^T as the B operand
-            uint32_t pb[2][kNT][2];
+            uint32_t pb[kTiles][kNT][2];
 #pragma unroll
             for (int n = 0; n < kNT; ++n) {
+                // a row without a key yet: 2^-inf is 0
                 const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0];
                 const float m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
 #pragma unroll
-                for (int a = 0; a < 2; ++a)
+                for (int a = 0; a < kTiles; ++a)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float p0 = ex2_approx(s[a][n][2 * e] - m0);
-                        const float p1 = ex2_approx(s[a][n][2 * e + 1] - m1);
+                        const float p0 = ex2_approx(fmaf(s[a][n][2 * e], f[n][0], -m0));
+                        const float p1 = ex2_approx(fmaf(s[a][n][2 * e + 1], f[n][1], -m1));
                         l[n][0] += p0;
                         l[n][1] += p1;
                         pb[a][n][e] = transpose8x8(f16x2_of(p0, p1));
@@ -721,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
             }
             // O^T += V^T P^T
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+            for (int a = 0; a < kTiles; ++a)
 #pragma unroll
                 for (int u = 0; u < NU; ++u) {
                     uint32_t vw[4][VU / 8], sc[2];
@@ -753,14 +796,20 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
                         }
                     }
                 }
-            pos0 = pos1;
-            pos1 = pos2;
+#pragma unroll
+            for (int i = 0; i + 1 < kStages; ++i)
+#pragma unroll
+                for (int j = 0; j < kSets; ++j)
+                    pos[i][j] = pos[i + 1][j];
+            __syncwarp();                                          // the block's stage is free
         }
         // after a wait that ran out: the copies still on their way land before the CTA goes on
-        if (kBulk && blk < b_hi) {
-            wait_drain(&bars[at], phase);
-            if (blk + kWarps < b_hi)
-                wait_drain(&bars[after(at)], phase ^ (at == kStages - 1));
+        for (int s = at, ph = phase; kBulk && blk < b_hi; blk += kWarps) {
+            wait_drain(&bars[s], ph);
+            ph ^= s == kStages - 1;
+            s = after(s);
+            if (s == at)
+                break;
         }
         cp_async_wait_all();
         __syncthreads();                                     // the staging becomes the join's buffer

@@ -412,6 +412,7 @@ struct CattnPlan {
     int tile_rows, tiles, rows, splits;
     long long works;
     size_t workspace;
+    int chunk;              // keys that are shared out together
     int ctas;               // of the register kernel: those that share the chunks, 0: one a row tile
     CattnFn fn;
     CattnWideFn wide_fn;
@@ -431,10 +432,12 @@ void cattn_pick(CattnPlan *pl)
         pl->fn = pl->bulk ? cache_attn_kernel<kDk, kDv, 1, true> : cache_attn_kernel<kDk, kDv, 1, false>;
         pl->smem = Shape<kDk, kDv, 1>::kSmem;
         pl->ctas = Shape<kDk, kDv, 1>::kCtas;
+        pl->chunk = Shape<kDk, kDv, 1>::kChunk;
     } else {
         pl->fn = pl->bulk ? cache_attn_kernel<kDk, kDv, 2, true> : cache_attn_kernel<kDk, kDv, 2, false>;
         pl->smem = Shape<kDk, kDv, 2>::kSmem;
         pl->ctas = Shape<kDk, kDv, 2>::kCtas;
+        pl->chunk = Shape<kDk, kDv, 2>::kChunk;
     }
 }
 
@@ -518,7 +521,7 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
     } else {
         // as many CTAs as the GPU holds share the chunks; where no tile has more
         // than one chunk, a CTA each, and nothing to join
-        const long long chunks = (most + csa::cattn::kChunk - 1) / csa::cattn::kChunk;
+        const long long chunks = (most + pl->chunk - 1) / pl->chunk;
         const long long held = static_cast<long long>(sms) * pl->ctas;
         pl->ctas = chunks <= 1 ? 0 : static_cast<int>(pl->works * chunks < held ? pl->works * chunks : held);
     }
@@ -633,6 +636,7 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     p.wait_limit = static_cast<long long>(g_wait_limit);
     p.splits = pl.splits;
     p.ctas = pl.ctas;
+    p.chunk = pl.chunk;
     p.works = static_cast<int>(pl.works / a->B);
     p.tiles = pl.tiles;
     p.rows = pl.rows;
