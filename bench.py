@@ -52,7 +52,10 @@ def load_peaks():
 
 
 # sources of the consumer kernels, which the indexer step does not build on
-CONSUMER_SOURCES = ("sparse_attn_kernel.cuh", "union_kernel.cuh")
+CONSUMER_SOURCES = ("sparse_attn_kernel.cuh", "union_kernel.cuh", "cache_attn_join_kernel.cuh",
+                    "cache_attn_kernel.cuh", "cache_attn_unit.cu", "cache_attn_unit.cuh",
+                    "cache_attn_wide_kernel.cuh", "cache_common.cuh", "cache_host.cuh",
+                    "cache_rows_kernel.cuh", "rotary_kernel.cuh")
 
 
 def kernel_sources_sha() -> str:

@@ -1,0 +1,128 @@
+// cache_attn_join_kernel.cuh -- the second kernels of attention over a 4-bit
+// cache: what several CTAs found for one row tile becomes the rows' outputs.
+#pragma once
+#include "cache_attn_kernel.cuh"
+
+namespace csa {
+namespace cattn {
+
+// Joins the pieces of the row tiles that several CTAs of the kernel above share: out =
+// sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.  A block takes rows of sequence
+// blockIdx.x, its warps every fourth piece of a row.
+__global__ void __launch_bounds__(kThreads) cache_attn_pieces_kernel(const AttnParams p, int Dv, int tile_rows)
+{
+    __shared__ long long scratch[kWarps];
+    __shared__ float part[kWarps][256 + 2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.x;
+    const int all = chunks_of(p, b);
+    if (all == 0)
+        return;                                          // written by the kernel above
+    const long long total = chunks_before(p, p.B, scratch), first = chunks_before(p, b, scratch);
+    const int ctas = static_cast<int>(min(static_cast<long long>(p.ctas), total));
+    for (int row = blockIdx.y; row < p.S * p.HA; row += gridDim.y) {
+        const int i = row / p.HA, head = row - i * p.HA, h = head / p.G;
+        const int r = p.idx ? head - h * p.G : i * p.G + head - h * p.G;
+        const int w = ((p.idx ? i * p.H : 0) + h) * p.tiles + r / tile_rows;
+        const long long start = first + static_cast<long long>(w) * all;
+        const int k0 = cta_of(start, total, ctas), k1 = cta_of(start + all - 1, total, ctas);
+        if (k0 == k1)
+            continue;                                    // one CTA had the whole tile
+        const long long stride = static_cast<long long>(tile_rows) * (Dv + 2);
+        // the first CTA's piece begins the tile (its second slot), the others' end or fill it
+        auto piece = [&](int k) {
+            return p.part + (2ll * k + (k == k0 ? 1 : 0)) * stride + (r % tile_rows) * (Dv + 2);
+        };
+        float top = -INFINITY;
+        for (int k = k0 + threadIdx.x; k <= k1; k += kThreads)
+            top = fmaxf(top, piece(k)[Dv]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        __syncthreads();                                 // (the row before has been read)
+        if (lane == 0)
+            part[warp][256] = top;
+        __syncthreads();
+        top = fmaxf(fmaxf(part[0][256], part[1][256]), fmaxf(part[2][256], part[3][256]));
+        const float base = top == -INFINITY ? 0.0f : top;
+        float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
+#pragma unroll 4
+        for (int k = k0 + warp; k <= k1; k += kWarps) {
+            const float *src = piece(k);
+            const float a = ex2_approx(src[Dv] - base);
+            sum += a * src[Dv + 1];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (64 * j < Dv) {
+                    const float2 v = *reinterpret_cast<const float2 *>(src + 64 * j + 2 * lane);
+                    x[2 * j] += a * v.x;
+                    x[2 * j + 1] += a * v.y;
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (64 * j < Dv)
+                *reinterpret_cast<float2 *>(&part[warp][64 * j + 2 * lane]) = make_float2(x[2 * j], x[2 * j + 1]);
+        if (lane == 0)
+            part[warp][257] = sum;
+        __syncthreads();
+        sum = part[0][257] + part[1][257] + part[2][257] + part[3][257];
+        const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
+        const long long out_row = static_cast<long long>(b) * p.S * p.HA + row;
+        for (int d = 2 * threadIdx.x; d < Dv; d += 2 * kThreads) {
+            const float u = part[0][d] + part[1][d] + part[2][d] + part[3][d];
+            const float v = part[0][d + 1] + part[1][d + 1] + part[2][d + 1] + part[3][d + 1];
+            *reinterpret_cast<uint32_t *>(p.out + out_row * Dv + d) = cache::bf16x2_of(u * inv, v * inv);
+        }
+        if (p.lse && threadIdx.x == 0)
+            p.lse[out_row] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
+// Joins the wide kernel's shares of one row, one warp a row.
+__global__ void __launch_bounds__(128) cache_attn_join_kernel(const AttnParams p, int Dv, int tile_rows,
+                                                              long long rows)
+{
+    const int lane = threadIdx.x & 31;
+    const long long at = blockIdx.x * 4ll + (threadIdx.x >> 5);   // (b, i, head)
+    if (at >= rows)
+        return;
+    const int head = static_cast<int>(at % p.HA);
+    const long long bi = at / p.HA;
+    const int h = head / p.G;
+    const int r = p.idx ? head - h * p.G : static_cast<int>(bi % p.S) * p.G + head - h * p.G;
+    const long long group = p.idx ? bi * p.H + h : bi / p.S * p.H + h;
+    const long long work = group * p.tiles + r / tile_rows;
+    const long long stride = static_cast<long long>(tile_rows) * (Dv + 2);
+    const float *src = p.part + work * p.splits * stride + (r % tile_rows) * (Dv + 2);
+    float top = -INFINITY;
+    for (int s = lane; s < p.splits; s += 32)
+        top = fmaxf(top, src[s * stride + Dv]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float sum = 0.0f;
+    if (top != -INFINITY)
+        for (int s = lane; s < p.splits; s += 32)
+            sum += ex2_approx(src[s * stride + Dv] - top) * src[s * stride + Dv + 1];
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
+    for (int d = 2 * lane; d < Dv; d += 64) {
+        float x = 0.0f, y = 0.0f;
+        if (top != -INFINITY)
+            for (int s = 0; s < p.splits; ++s) {
+                const float a = ex2_approx(src[s * stride + Dv] - top);
+                const float2 v = *reinterpret_cast<const float2 *>(src + s * stride + d);
+                x += a * v.x;
+                y += a * v.y;
+            }
+        *reinterpret_cast<uint32_t *>(p.out + at * Dv + d) = cache::bf16x2_of(x * inv, y * inv);
+    }
+    if (p.lse && lane == 0)
+        p.lse[at] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+} // namespace cattn
+} // namespace csa

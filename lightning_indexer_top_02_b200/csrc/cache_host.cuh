@@ -4,8 +4,8 @@
 #include <cmath>
 
 #include "csa_cache.h"
-#include "cache_attn_kernel.cuh"
-#include "cache_attn_wide_kernel.cuh"
+#include "cache_attn_join_kernel.cuh"
+#include "cache_attn_unit.cuh"
 #include "cache_rows_kernel.cuh"
 #include "rotary_kernel.cuh"
 
@@ -402,56 +402,7 @@ extern "C" csa_status_t csa_cache_read(const csa_cache_read_args_t *args, cudaSt
 // Attention over a 4-bit cache.
 namespace {
 
-using CattnFn = void (*)(const csa::cattn::AttnParams);
-using CattnWideFn = void (*)(const csa::cattn::WideParams);
-
-struct CattnPlan {
-    bool wide;
-    bool bulk;              // tiles of 16 keys lie together in a page (the register kernel)
-    int keys, raw;          // of the wide kernel: keys of a tile, staging bytes
-    int tile_rows, tiles, rows, splits;
-    long long works;
-    size_t workspace;
-    int chunk;              // keys that are shared out together
-    int ctas;               // of the register kernel: those that share the chunks, 0: one a row tile
-    CattnFn fn;
-    CattnWideFn wide_fn;
-    int smem;
-};
-
-template <int kDk, int kDv>
-void cattn_pick(CattnPlan *pl)
-{
-    using namespace csa::cattn;
-    if (pl->wide) {
-        pl->keys = WideShape<kDk, kDv>::kKeys;
-        pl->raw = 2 * kGatherWarps * WideShape<kDk, kDv>::kRaw;
-        pl->wide_fn = pl->tile_rows == kWideRows ? cache_attn_wide_kernel<kDk, kDv, false>
-                                                 : cache_attn_wide_kernel<kDk, kDv, true>;
-    } else if (pl->tile_rows == 8) {
-        pl->fn = pl->bulk ? cache_attn_kernel<kDk, kDv, 1, true> : cache_attn_kernel<kDk, kDv, 1, false>;
-        pl->smem = Shape<kDk, kDv, 1>::kSmem;
-        pl->ctas = Shape<kDk, kDv, 1>::kCtas;
-        pl->chunk = Shape<kDk, kDv, 1>::kChunk;
-    } else {
-        pl->fn = pl->bulk ? cache_attn_kernel<kDk, kDv, 2, true> : cache_attn_kernel<kDk, kDv, 2, false>;
-        pl->smem = Shape<kDk, kDv, 2>::kSmem;
-        pl->ctas = Shape<kDk, kDv, 2>::kCtas;
-        pl->chunk = Shape<kDk, kDv, 2>::kChunk;
-    }
-}
-
-template <int kDk>
-bool cattn_pick_dv(int dv, CattnPlan *pl)
-{
-    switch (dv) {
-    case 64: cattn_pick<kDk, 64>(pl); return true;
-    case 128: cattn_pick<kDk, 128>(pl); return true;
-    case 192: cattn_pick<kDk, 192>(pl); return true;
-    case 256: cattn_pick<kDk, 256>(pl); return true;
-    }
-    return false;
-}
+using csa::cattn::CattnPlan;
 
 csa_status_t validate_cattn(const csa_cache_attn_args_t *a)
 {
@@ -497,10 +448,10 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
     pl->works = static_cast<long long>(a->B) * (a->idx ? a->S : 1) * H * pl->tiles;
     bool ok = false;
     switch (a->cache_k.D) {
-    case 64: ok = cattn_pick_dv<64>(a->cache_v.D, pl); break;
-    case 128: ok = cattn_pick_dv<128>(a->cache_v.D, pl); break;
-    case 192: ok = cattn_pick_dv<192>(a->cache_v.D, pl); break;
-    case 256: ok = cattn_pick_dv<256>(a->cache_v.D, pl); break;
+    case 64: ok = csa::cattn::pick_64(a->cache_v.D, pl); break;
+    case 128: ok = csa::cattn::pick_128(a->cache_v.D, pl); break;
+    case 192: ok = csa::cattn::pick_192(a->cache_v.D, pl); break;
+    case 256: ok = csa::cattn::pick_256(a->cache_v.D, pl); break;
     }
     if (!ok)
         return CSA_ERR_UNSUPPORTED;

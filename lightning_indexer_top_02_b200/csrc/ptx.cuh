@@ -63,9 +63,9 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity, bo
     return ok != 0;
 }
 
-// Device error word (per device, per loaded library): [0] = error code,
-// [1] = where (role), [2] = work item, [3] = detail.
-__device__ int g_csa_error[4];
+// Device error word (per device, per translation unit of the loaded library):
+// [0] = error code, [1] = where (role), [2] = work item, [3] = detail.
+static __device__ int g_csa_error[4];
 
 enum : int { kErrTimeout = 5 };
 
