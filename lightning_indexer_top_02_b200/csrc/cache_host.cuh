@@ -214,13 +214,19 @@ extern "C" csa_status_t csa_rotary(const csa_rotary_args_t *args, cudaStream_t s
     const bool inter = a->interleaved != 0;
     const int wide = 16 / size;
     const int v = rotary_fits(a, wide) ? wide : 1;
-    p.pair_units = inter ? (v > 1 ? a->rot_dim / v : p.half) : p.half / v;
-    p.units = p.pair_units + (p.copy ? (a->D - a->rot_dim) / v : 0);
+    if (inter && v > 1) {
+        p.units = (p.copy ? a->D : a->rot_dim) / v;
+    } else {
+        const int rest = (a->D - a->rot_dim) / v;
+        p.pair_units = p.half / v;
+        p.units = p.pair_units + (p.copy ? (rest + 1) / 2 : 0);
+    }
     p.div_units = FastDiv::of(p.units);
-    // blocks: about eight units a thread; a token's heads are shared out when
+    p.div_half = FastDiv::of(p.half);
+    // blocks: about four units a thread; a token's heads are shared out when
     // there are too few tokens to fill the GPU
     const long long per_token = static_cast<long long>(a->H) * p.units;
-    const long long want = 8ll * csa::rotary::kThreads;
+    const long long want = 4ll * csa::rotary::kThreads;
     long long tokens = per_token >= want ? 1 : want / per_token;
     while (tokens > 1 && (a->N + tokens - 1) / tokens < 4ll * sms)
         tokens = (tokens + 1) / 2;
@@ -260,10 +266,11 @@ template <int kType>
 void launch_append(const csa::cache::AppendParams &p, bool inter, unsigned grid, size_t smem,
                    cudaStream_t stream)
 {
-    if (inter)
-        csa::cache::append_kernel<kType, true><<<grid, csa::cache::kRowThreads, smem, stream>>>(p);
-    else
-        csa::cache::append_kernel<kType, false><<<grid, csa::cache::kRowThreads, smem, stream>>>(p);
+    using namespace csa::cache;
+    auto fn = p.half == 0 ? append_kernel<kType, kStill>
+              : inter     ? append_kernel<kType, kInterleaved>
+              : ((p.off | p.half) & 15) == 0 ? append_kernel<kType, kWhole> : append_kernel<kType, kHalves>;
+    fn<<<grid, kRowThreads, smem, stream>>>(p);
 }
 
 } // namespace
@@ -332,11 +339,14 @@ extern "C" csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStre
     tokens = tokens < 1 ? 1 : tokens > csa::cache::kMaxTile ? csa::cache::kMaxTile : tokens;
     while (tokens > 1 && (a->N + tokens - 1) / tokens < 4 * sms)
         tokens = (tokens + 1) / 2;
-    if (p.half && tokens > 2048 / p.half)                // cos and sin in 32 KB
-        tokens = 2048 / p.half;
+    const int turns = p.half + (p.half >> 3);            // places of a token's cos and sin (turn_at)
+    if (p.half && tokens > 2048 / turns)                 // in 32 KB
+        tokens = 2048 / turns;
     p.tokens = tokens;
+    p.div_H = FastDiv::of(p.H);
+    p.div_half = FastDiv::of(p.half ? p.half : 1);
     const unsigned grid = static_cast<unsigned>((static_cast<long long>(a->N) + tokens - 1) / tokens);
-    const size_t smem = static_cast<size_t>(tokens) * p.half * sizeof(csa::cache::Turn);
+    const size_t smem = static_cast<size_t>(tokens) * turns * sizeof(csa::cache::Turn);
     const bool inter = a->interleaved != 0;
     if (!mark(0, stream))
         return CSA_ERR_CUDA;
@@ -366,7 +376,7 @@ extern "C" csa_status_t csa_cache_read(const csa_cache_read_args_t *args, cudaSt
         return st;
     if (!a->out || !aligned(a->out, 16))
         return CSA_ERR_INVALID_ARG;
-    if (a->T >= kIntLimit)
+    if (static_cast<long long>(a->T) * a->cache.H >= kIntLimit / 2)
         return CSA_ERR_UNSUPPORTED;
     const int sms = device_sms();
     if (sms <= 0)
@@ -381,11 +391,13 @@ extern "C" csa_status_t csa_cache_read(const csa_cache_read_args_t *args, cudaSt
     p.H = a->cache.H;
     p.D = a->cache.D;
     p.lanes = row_lanes(p.D);
-    p.rows = static_cast<long long>(a->B) * a->T * p.H;
+    p.rows = a->T * p.H;
+    p.div_H = FastDiv::of(p.H);
     p.out = static_cast<__nv_bfloat16 *>(a->out);
-    const int per = csa::cache::kRowThreads / p.lanes;
-    const long long need = (p.rows + per - 1) / per, most = 64ll * sms;
-    const unsigned grid = static_cast<unsigned>(need < most ? need : most);
+    const int per = csa::cache::kRowThreads / p.lanes * csa::cache::kReadAhead;
+    const unsigned rows_y = a->B < 65535 ? a->B : 65535;
+    long long need = (static_cast<long long>(p.rows) + per - 1) / per, most = (64ll * sms + rows_y - 1) / rows_y;
+    const dim3 grid(static_cast<unsigned>(need < most ? need : most), rows_y);
     if (!mark(0, stream))
         return CSA_ERR_CUDA;
     if (a->cache.dtype == CSA_CACHE_BF16)

@@ -12,6 +12,7 @@ namespace cache {
 
 constexpr int kRowThreads = 128;
 constexpr int kMaxTile = 32;             // tokens a block takes at most
+constexpr int kReadAhead = 2;           // rows a lane loads before it works on the first (read)
 
 struct AppendParams {
     const __nv_bfloat16 *k, *v;
@@ -26,6 +27,7 @@ struct AppendParams {
     float rope_scale;
     int tokens;                          // tokens a block takes
     int lanes_k, lanes_v;                // lanes a row takes (2^n >= D / 16)
+    FastDiv div_H, div_half;
 };
 
 // cos and sin of one pair, in 40 bits: the high part has 16 bits, so its
@@ -33,6 +35,10 @@ struct AppendParams {
 struct Turn {
     float ch, cl, sh, sl;
 };
+
+// Where pair i's turn lies in shared memory: one place is left out after eight, so that
+// lanes 8 or 16 pairs apart do not meet in a bank.
+__device__ __forceinline__ int turn_at(int i) { return i + (i >> 3); }
 
 __device__ __forceinline__ Turn make_turn(int pos, float freq, float scale)
 {
@@ -61,19 +67,25 @@ __device__ __forceinline__ float turned(float a, float ch, float cl, float b, fl
     return __fadd_rn(sum, __fadd_rn(err, low));
 }
 
-// 16 consecutive bf16 elements as floats.
-__device__ __forceinline__ void load16(const __nv_bfloat16 *src, float (&x)[16])
-{
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src));
-    const uint4 b = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float2 f = float2_of_bf16x2(w[j]);
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
+// 16 consecutive bf16 elements.
+struct Raw16 {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *src)
+    {
+        a = __ldg(reinterpret_cast<const uint4 *>(src));
+        b = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
     }
-}
+    __device__ __forceinline__ void unpack(float (&x)[16]) const
+    {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 f = float2_of_bf16x2(w[j]);
+            x[2 * j] = f.x;
+            x[2 * j + 1] = f.y;
+        }
+    }
+};
 
 // Stores 16 elements of a row in the cache's type.  E4M3: every lane of the
 // row's group calls (peak is exchanged), `active` ones store.
@@ -131,36 +143,42 @@ __device__ __forceinline__ void store16(const CacheView &c, uint8_t *data, uint8
     }
 }
 
-// Rotates the 16 elements [e0, e0 + 16) of a head row; src is the row.
-template <bool kInter>
+// How rows are rotated: not at all; interleaved pairs; halves that lanes of 16 elements
+// take whole (offset and half multiples of 16: a lane's partners are 16 elements that
+// lie together); halves at any even place.
+enum Rotation : int { kStill = 0, kInterleaved = 1, kWhole = 2, kHalves = 3 };
+
+// Rotates the 16 elements [e0, e0 + 16) of a head row; src is the row, `partner` the
+// elements half a rotation away (kWhole).
+template <int kHow>
 __device__ __forceinline__ void rotate16(const __nv_bfloat16 *src, int e0, int off, int half,
-                                         const Turn *w, float (&x)[16])
+                                         const Turn *w, const Raw16 &partner, float (&x)[16])
 {
-    if (e0 + 16 <= off || e0 >= off + 2 * half)
+    if (kHow == kStill || e0 + 16 <= off || e0 >= off + 2 * half)
         return;
-    if constexpr (kInter) {
+    if constexpr (kHow == kInterleaved) {
         // off is even: a pair lies within the lane's elements
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
             const int i = (e0 + j - off) >> 1;
             if (i >= 0 && i < half) {
-                const Turn t = w[i];
+                const Turn t = w[turn_at(i)];
                 const float a = x[j], b = x[j + 1];
                 x[j] = turned(a, t.ch, t.cl, b, -t.sh, -t.sl);
                 x[j + 1] = turned(b, t.ch, t.cl, a, t.sh, t.sl);
             }
         }
-    } else if (((off | half) & 15) == 0) {
-        // the partners are another lane's 16 elements, read again (they are in L1)
+    } else if constexpr (kHow == kWhole) {
         const bool first = e0 < off + half;
         float y[16];
-        load16(src + (first ? e0 + half : e0 - half), y);
-        const Turn *u = w + (first ? e0 - off : e0 - off - half);
+        partner.unpack(y);
+        const int i0 = first ? e0 - off : e0 - off - half;      // a multiple of 16
+        const Turn *u = w + turn_at(i0);
+        const float sign = first ? -1.0f : 1.0f;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const Turn t = u[j];
-            x[j] = first ? turned(x[j], t.ch, t.cl, y[j], -t.sh, -t.sl)
-                         : turned(x[j], t.ch, t.cl, y[j], t.sh, t.sl);
+            const Turn t = u[turn_at(j)];
+            x[j] = turned(x[j], t.ch, t.cl, sign * y[j], t.sh, t.sl);
         }
     } else {
 #pragma unroll
@@ -168,7 +186,7 @@ __device__ __forceinline__ void rotate16(const __nv_bfloat16 *src, int e0, int o
             const int i = e0 + j - off;
             if (i >= 0 && i < 2 * half) {
                 const bool first = i < half;
-                const Turn t = w[first ? i : i - half];
+                const Turn t = w[turn_at(first ? i : i - half)];
                 const float b = __bfloat162float(src[first ? e0 + j + half : e0 + j - half]);
                 x[j] = first ? turned(x[j], t.ch, t.cl, b, -t.sh, -t.sl)
                              : turned(x[j], t.ch, t.cl, b, t.sh, t.sl);
@@ -177,31 +195,62 @@ __device__ __forceinline__ void rotate16(const __nv_bfloat16 *src, int e0, int o
     }
 }
 
-template <int kType, bool kInter, bool kRotate>
-__device__ __forceinline__ void append_rows(const __nv_bfloat16 *src, long long ts, long long hs, int D,
-                                            int lanes, const CacheView &c, const PageMap &pm, int H,
-                                            int n0, int nt, const int *page, const int *off,
-                                            const Turn *turns, int rope_off, int half)
-{
-    const int lane = threadIdx.x & (lanes - 1);
-    const int rows = nt * H;
-    const int step = kRowThreads / lanes;
-    const bool has = 16 * lane < D;
-    // every lane of a warp takes the same number of turns (store16 exchanges)
-    for (int r0 = 0; r0 < rows; r0 += step) {
-        const int r = r0 + threadIdx.x / lanes;
-        const int t = r < rows ? r / H : 0, h = r < rows ? r - t * H : 0;
-        const bool active = r < rows && has && page[t] >= 0;
+// A lane's part of one row on its way from K or V.
+struct RowPart {
+    Raw16 own, other;                    // 16 elements, and their partners (kWhole)
+    int tok, head;                       // head -1: none
+};
+
+// How a block goes through the rows of K, or of V: `lanes` lanes a row, round by round.
+template <int kHow>
+struct RowWalk {
+    const __nv_bfloat16 *src;
+    long long ts, hs;
+    int D, lanes, step, lane, rows, rounds, n0;
+    bool partnered;
+    int partner;
+
+    __device__ __forceinline__ RowWalk(const AppendParams &p, const __nv_bfloat16 *src_, long long ts_, long long hs_,
+                                       int D_, int lanes_, int n0_, int nt)
+        : src(src_), ts(ts_), hs(hs_), D(D_), lanes(lanes_), n0(n0_)
+    {
+        lane = threadIdx.x & (lanes - 1);
+        step = kRowThreads / lanes;
+        rows = nt * p.H;
+        rounds = (rows + step - 1) / step;
+        partnered = kHow == kWhole && 16 * lane >= p.off && 16 * lane < p.off + 2 * p.half;
+        partner = 16 * lane < p.off + p.half ? 16 * lane + p.half : 16 * lane - p.half;
+    }
+    __device__ __forceinline__ const __nv_bfloat16 *row(const RowPart &r) const
+    {
+        return src + (n0 + r.tok) * ts + r.head * hs;
+    }
+    __device__ __forceinline__ void load(const AppendParams &p, int round, RowPart &r) const
+    {
+        const int i = round * step + threadIdx.x / lanes;
+        r.tok = static_cast<int>(p.div_H.div(i < rows ? i : 0));
+        r.head = i < rows && 16 * lane < D ? i - r.tok * p.H : -1;
+        if (r.head >= 0) {
+            r.own.load(row(r) + 16 * lane);
+            if (partnered)
+                r.other.load(row(r) + partner);
+        }
+    }
+    // (every lane of a warp: store16 exchanges)
+    template <int kType>
+    __device__ __forceinline__ void work(const AppendParams &p, const CacheView &c, const RowPart &r, const int *page,
+                                         const int *off, const Turn *turns) const
+    {
         float x[16];
         uint8_t *data = nullptr, *scale = nullptr;
+        const int pg = page[r.tok];
+        const bool active = r.head >= 0 && pg >= 0;
         if (active) {
-            const __nv_bfloat16 *row = src + (n0 + t) * ts + h * hs;
-            load16(row + 16 * lane, x);
-            if (kRotate)
-                rotate16<kInter>(row, 16 * lane, rope_off, half, turns + t * half, x);
-            data = const_cast<uint8_t *>(row_data(c, pm, page[t], h, off[t]));
+            r.own.unpack(x);
+            rotate16<kHow>(row(r), 16 * lane, p.off, p.half, turns + r.tok * turn_at(p.half), r.other, x);
+            data = const_cast<uint8_t *>(row_data(c, p.pm, pg, r.head, off[r.tok]));
             if (kType != 0)
-                scale = const_cast<uint8_t *>(row_scale(c, pm, page[t], h, off[t]));
+                scale = const_cast<uint8_t *>(row_scale(c, p.pm, pg, r.head, off[r.tok]));
         } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -209,17 +258,22 @@ __device__ __forceinline__ void append_rows(const __nv_bfloat16 *src, long long 
         }
         store16<kType>(c, data, scale, lane, lanes, active, x);
     }
-}
+};
 
 // One block takes p.tokens tokens: their places (one thread a token), their
-// cos and sin, then every row of K and of V.
-template <int kType, bool kInter>
-__global__ void __launch_bounds__(kRowThreads) append_kernel(const AppendParams p)
+// cos and sin, then every row of K and of V.  A row's elements are loaded a round
+// before they are worked on, the first ones before their places are known.
+template <int kType, int kHow>
+__global__ void __launch_bounds__(kRowThreads, 8) append_kernel(const AppendParams p)
 {
     extern __shared__ Turn turns[];                     // [tokens][half]
     __shared__ int s_page[kMaxTile], s_off[kMaxTile], s_pos[kMaxTile];
     const int n0 = blockIdx.x * p.tokens;
     const int nt = min(p.tokens, p.N - n0);
+    const RowWalk<kHow> kw(p, p.k, p.kt, p.kh, p.Dk, p.lanes_k, n0, nt);
+    const RowWalk<kStill> vw(p, p.v, p.vt, p.vh, p.Dv, p.lanes_v, n0, nt);
+    RowPart cur, next;
+    kw.load(p, 0, cur);
     if (threadIdx.x < nt) {
         const int n = n0 + threadIdx.x;
         int b = -1, pos = -1, page = -1, off = 0;
@@ -248,20 +302,29 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const AppendParams 
         s_pos[threadIdx.x] = p.positions ? __ldg(p.positions + n) : pos;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nt * p.half; i += kRowThreads) {
-        const int t = i / p.half;
-        turns[i] = make_turn(s_pos[t], __ldg(p.inv_freq + i - t * p.half), p.rope_scale);
+    if constexpr (kHow != kStill) {
+        for (int i = threadIdx.x; i < nt * p.half; i += kRowThreads) {
+            const int t = static_cast<int>(p.div_half.div(i)), f = i - t * p.half;
+            turns[t * turn_at(p.half) + turn_at(f)] = make_turn(s_pos[t], __ldg(p.inv_freq + f), p.rope_scale);
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    if (p.half)
-        append_rows<kType, kInter, true>(p.k, p.kt, p.kh, p.Dk, p.lanes_k, p.ck, p.pm, p.H, n0, nt,
-                                         s_page, s_off, turns, p.off, p.half);
-    else
-        append_rows<kType, kInter, false>(p.k, p.kt, p.kh, p.Dk, p.lanes_k, p.ck, p.pm, p.H, n0, nt,
-                                          s_page, s_off, turns, 0, 0);
-    if (p.v)
-        append_rows<kType, kInter, false>(p.v, p.vt, p.vh, p.Dv, p.lanes_v, p.cv, p.pm, p.H, n0, nt,
-                                          s_page, s_off, turns, 0, 0);
+    for (int i = 0; i < kw.rounds; ++i) {
+        if (i + 1 < kw.rounds)
+            kw.load(p, i + 1, next);
+        else if (p.v)
+            vw.load(p, 0, next);
+        kw.template work<kType>(p, p.ck, cur, s_page, s_off, turns);
+        cur = next;
+    }
+    if (!p.v)
+        return;
+    for (int i = 0; i < vw.rounds; ++i) {
+        if (i + 1 < vw.rounds)
+            vw.load(p, i + 1, next);
+        vw.template work<kType>(p, p.cv, cur, s_page, s_off, turns);
+        cur = next;
+    }
 }
 
 // ---------------------------------------------------------------- read back
@@ -272,11 +335,73 @@ struct ReadParams {
     const int32_t *kv_len;
     int B, T, H, D;
     int lanes;
-    long long rows;                      // B * T * H
+    int rows;                            // T * H, of one sequence
+    FastDiv div_H;
     __nv_bfloat16 *out;                  // [B, T, H, D]
 };
 
-// A group of lanes takes a row at a time; a lane writes 16 elements.
+// 16 stored elements: the codes, and the scale they share.
+template <int kType>
+struct Held16 {
+    uint4 a, b;                          // kType 1: a; 2: a.x, a.y
+    float s;
+    uint32_t s8;
+
+    __device__ __forceinline__ void load(const uint8_t *data, const uint8_t *scale, int lane)
+    {
+        if constexpr (kType == 0) {
+            a = __ldg(reinterpret_cast<const uint4 *>(data) + 2 * lane);
+            b = __ldg(reinterpret_cast<const uint4 *>(data) + 2 * lane + 1);
+        } else if constexpr (kType == 1) {
+            a = __ldg(reinterpret_cast<const uint4 *>(data) + lane);
+            s = __ldg(reinterpret_cast<const float *>(scale));
+        } else {
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(data) + lane);
+            a.x = w.x;
+            a.y = w.y;
+            s8 = __ldg(scale + lane);
+        }
+    }
+
+    __device__ __forceinline__ void store(uint4 *dst, float tensor_scale) const
+    {
+        uint4 w[2];
+        uint32_t *u = reinterpret_cast<uint32_t *>(w);
+        if constexpr (kType == 0) {
+            w[0] = a;
+            w[1] = b;
+        } else if constexpr (kType == 1) {
+            const uint32_t q[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 lo = float2_of_f16x2(f16x2_of_e4m3x2(q[j] & 0xFFFFu));
+                const float2 hi = float2_of_f16x2(f16x2_of_e4m3x2(q[j] >> 16));
+                u[2 * j] = bf16x2_of(lo.x * s, lo.y * s);
+                u[2 * j + 1] = bf16x2_of(hi.x * s, hi.y * s);
+            }
+        } else {
+            const float f = float2_of_f16x2(f16x2_of_e4m3x2(s8)).x * tensor_scale;
+            const uint32_t q[2] = {a.x, a.y};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float2 f0 = float2_of_f16x2(f16x2_of_e2m1x2<0>(q[j]));
+                const float2 f1 = float2_of_f16x2(f16x2_of_e2m1x2<1>(q[j]));
+                const float2 f2 = float2_of_f16x2(f16x2_of_e2m1x2<2>(q[j]));
+                const float2 f3 = float2_of_f16x2(f16x2_of_e2m1x2<3>(q[j]));
+                u[4 * j] = bf16x2_of(f0.x * f, f0.y * f);
+                u[4 * j + 1] = bf16x2_of(f1.x * f, f1.y * f);
+                u[4 * j + 2] = bf16x2_of(f2.x * f, f2.y * f);
+                u[4 * j + 3] = bf16x2_of(f3.x * f, f3.y * f);
+            }
+        }
+        dst[0] = w[0];
+        dst[1] = w[1];
+    }
+};
+
+// Rows of sequences blockIdx.y, + gridDim.y, ..: a group of lanes takes kReadAhead
+// rows at a time (all their loads are on the way before the first is used), a lane
+// writes 16 elements of each.
 template <int kType>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p)
 {
@@ -284,52 +409,46 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p)
     const int per = kRowThreads / p.lanes;
     if (16 * lane >= p.D)
         return;
-    for (long long r = static_cast<long long>(blockIdx.x) * per + threadIdx.x / p.lanes; r < p.rows;
-         r += static_cast<long long>(gridDim.x) * per) {
-        const long long bt = r / p.H;
-        const int h = static_cast<int>(r - bt * p.H);
-        const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt - static_cast<long long>(b) * p.T);
-        int page, off;
-        uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-        if (t < __ldg(p.kv_len + b) && p.pm.locate(p.pm.table + b * p.pm.table_stride, t, page, off)) {
-            const uint8_t *data = row_data(p.c, p.pm, page, h, off);
-            uint32_t *u = reinterpret_cast<uint32_t *>(w);
-            if constexpr (kType == 0) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(data + 32 * lane);
-                w[0] = src[0];
-                w[1] = src[1];
-            } else if constexpr (kType == 1) {
-                const uint4 q = *reinterpret_cast<const uint4 *>(data + 16 * lane);
-                const float s = *reinterpret_cast<const float *>(row_scale(p.c, p.pm, page, h, off));
-                const uint32_t q4[4] = {q.x, q.y, q.z, q.w};
+    for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
+        const int len = __ldg(p.kv_len + b);
+        const int32_t *table = p.pm.table + b * p.pm.table_stride;
+        uint4 *out = reinterpret_cast<uint4 *>(p.out + static_cast<long long>(b) * p.rows * p.D);
+        const unsigned stride = gridDim.x * per;
+        for (unsigned r0 = blockIdx.x * per * kReadAhead + threadIdx.x / p.lanes; r0 < p.rows;
+             r0 += stride * kReadAhead) {
+            int t[kReadAhead], page[kReadAhead];
+            bool has[kReadAhead];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 lo = float2_of_f16x2(f16x2_of_e4m3x2(q4[j] & 0xFFFFu));
-                    const float2 hi = float2_of_f16x2(f16x2_of_e4m3x2(q4[j] >> 16));
-                    u[2 * j] = bf16x2_of(lo.x * s, lo.y * s);
-                    u[2 * j + 1] = bf16x2_of(hi.x * s, hi.y * s);
-                }
-            } else {
-                const uint2 q = *reinterpret_cast<const uint2 *>(data + 8 * lane);
-                const float s = float2_of_f16x2(f16x2_of_e4m3x2(
-                                    row_scale(p.c, p.pm, page, h, off)[lane])).x * p.c.tensor_scale;
-                const uint32_t q2[2] = {q.x, q.y};
+            for (int k = 0; k < kReadAhead; ++k) {
+                const unsigned r = r0 + k * per;
+                t[k] = static_cast<int>(p.div_H.div(min(r, static_cast<unsigned>(p.rows - 1))));
+                const int n = static_cast<int>(p.pm.div.div(t[k]));
+                has[k] = r < p.rows && t[k] < len && n < p.pm.max_pages;
+                page[k] = has[k] ? __ldg(table + n) : -1;
+            }
+            Held16<kType> x[kReadAhead];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float2 f0 = float2_of_f16x2(f16x2_of_e2m1x2<0>(q2[j]));
-                    const float2 f1 = float2_of_f16x2(f16x2_of_e2m1x2<1>(q2[j]));
-                    const float2 f2 = float2_of_f16x2(f16x2_of_e2m1x2<2>(q2[j]));
-                    const float2 f3 = float2_of_f16x2(f16x2_of_e2m1x2<3>(q2[j]));
-                    u[4 * j] = bf16x2_of(f0.x * s, f0.y * s);
-                    u[4 * j + 1] = bf16x2_of(f1.x * s, f1.y * s);
-                    u[4 * j + 2] = bf16x2_of(f2.x * s, f2.y * s);
-                    u[4 * j + 3] = bf16x2_of(f3.x * s, f3.y * s);
+            for (int k = 0; k < kReadAhead; ++k) {
+                has[k] = page[k] >= 0 && page[k] < p.pm.num_pages;
+                const int h = static_cast<int>(r0 + k * per) - t[k] * p.H;
+                const int off = t[k] - static_cast<int>(p.pm.div.div(t[k])) * p.pm.page_size;
+                if (has[k])
+                    x[k].load(row_data(p.c, p.pm, page[k], h, off), row_scale(p.c, p.pm, page[k], h, off), lane);
+            }
+#pragma unroll
+            for (int k = 0; k < kReadAhead; ++k) {
+                const unsigned r = r0 + k * per;
+                if (r >= p.rows)
+                    break;
+                uint4 *dst = out + (static_cast<long long>(r) * p.D + 16 * lane) / 8;
+                if (has[k]) {
+                    x[k].store(dst, p.c.tensor_scale);
+                } else {
+                    dst[0] = make_uint4(0u, 0u, 0u, 0u);
+                    dst[1] = make_uint4(0u, 0u, 0u, 0u);
                 }
             }
         }
-        uint4 *dst = reinterpret_cast<uint4 *>(p.out + r * p.D + 16 * lane);
-        dst[0] = w[0];
-        dst[1] = w[1];
     }
 }
 
