@@ -169,20 +169,23 @@ def _cache_struct(name: str, c: Cache) -> CsaCache:
                     _page_stride(name + ".data", data), _page_stride(name + ".scale", scale), c.tensor_scale)
 
 
-def _on(dev, **tensors):
-    """Every tensor (a cache: its two) on one CUDA device, and none that would need a gradient."""
+def _on(dev, names, *tensors):
+    """Every tensor on one CUDA device, and none that would need a gradient.  (Checked
+    in one go, names looked up only for an error: this is on every call's path.)"""
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or t.requires_grad):
+            break
+    else:
+        if dev >= 0:
+            return
     import torch
 
-    grad = torch.is_grad_enabled()
-    for name, t in tensors.items():
+    for name, t in zip(names.split(), tensors):
         if t is None:
-            continue
-        if isinstance(t, Cache):
-            _on(dev, **{name + ".data": t.data, name + ".scale": t.scale})
             continue
         if t.get_device() != dev or dev < 0:
             raise ValueError(f"{name} must be on " + (f"CUDA device {dev}" if dev >= 0 else "a CUDA device"))
-        if grad and t.requires_grad:
+        if t.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"{name} needs a gradient, which this call does not record")
 
 
@@ -222,26 +225,21 @@ def _elsewhere(device, stream):
         yield
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _launch(t, stream):
     """The call's stream handle, and a context in which the tensor's device is
     current and allocations belong to that stream (memory handed out on another one
-    could still be in use there); None where both already are."""
+    could still be in use there)."""
     import torch
 
     dev = t.get_device()
-    here = torch.cuda.current_stream(dev) if stream is not None or dev != torch.cuda.current_device() else None
-    if here is None:
-        return torch._C._cuda_getCurrentRawStream(dev), None
     if stream is None:
-        stream = here
+        if dev == torch.cuda.current_device():
+            return torch._C._cuda_getCurrentRawStream(dev), _HERE
+        stream = torch.cuda.current_stream(dev)
     return stream.cuda_stream, _elsewhere(dev, stream)
-
-
-def _within(ctx, fn, *args, **kw):
-    if ctx is None:
-        return fn(*args, **kw)
-    with ctx:
-        return fn(*args, **kw)
 
 
 def _check(status, what):
@@ -273,7 +271,7 @@ def rotary(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = F
     place).  ``inverse`` rotates back: the gradient."""
     import torch
 
-    kind = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(x.dtype)
+    kind = 0 if x.dtype == torch.bfloat16 else 1 if x.dtype == torch.float16 else 2 if x.dtype == torch.float32 else None
     shape = x.shape
     if kind is None or len(shape) < 2:
         raise TypeError("x must be a bfloat16, float16 or float32 tensor [..., H, D]")
@@ -283,20 +281,20 @@ def rotary(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = F
     xs = _token_strides("x", x)
     if out is not None and (out.shape != shape or out.dtype != x.dtype):
         raise TypeError("out must have the shape and type of x")
-    _on(dev, x=x, positions=positions, inv_freq=inv_freq, out=out)
+    _on(dev, "x positions inv_freq out", x, positions, inv_freq, out)
     s, ctx = _launch(x, stream)
-
-    def call(out):
+    with ctx:
         if out is None:
-            out = torch.empty(shape, dtype=x.dtype, device=x.device)
+            out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
         if x.numel():
             os = xs if out is x else _token_strides("out", out)
-            _check(csa_rotary(CsaRotaryArgs(x.data_ptr(), out.data_ptr(), kind, positions.numel(), shape[-2], shape[-1],
-                                            *xs, *os, pos, freq, 2 * inv_freq.numel(), rot_offset,
-                                            bool(interleaved), bool(inverse), scale), s), "csa_rotary")
-        return out
-
-    return _within(ctx, call, out)
+            st = L.load_library().csa_rotary(
+                ctypes.byref(CsaRotaryArgs(x.data_ptr(), out.data_ptr(), kind, positions.numel(), shape[-2], shape[-1],
+                                           *xs, *os, pos, freq, 2 * inv_freq.numel(), rot_offset, bool(interleaved),
+                                           bool(inverse), scale)), s)
+            if st:
+                raise L.CsaError(st, "csa_rotary")
+    return out
 
 
 def _token_strides(name, x):
@@ -350,12 +348,16 @@ def cache_append(k, cache_k: Cache, page_table, kv_len, *, v=None, cache_v: Opti
     cu = _int32("cu_tokens", cu_tokens, (B + 1,)) if cu_tokens is not None else None
     pos = _int32("positions", positions, lead) if positions is not None else None
     freq, rot = (_freq(inv_freq), 2 * inv_freq.numel()) if inv_freq is not None else (None, 0)
-    _on(dev, k=k, cache_k=cache_k, v=v, cache_v=cache_v, page_table=page_table, kv_len=kv_len, cu_tokens=cu_tokens,
-        positions=positions, inv_freq=inv_freq)
+    _on(dev, "k cache_k.data cache_k.scale v cache_v.data cache_v.scale page_table kv_len cu_tokens positions inv_freq",
+        k, cache_k.data, cache_k.scale, v, cache_v and cache_v.data, cache_v and cache_v.scale, page_table, kv_len,
+        cu_tokens, positions, inv_freq)
     a = CsaAppendArgs(kp, vp, *ks, *vs, N, B, S, cu, *pages, kc, vc, freq, pos, rot, rot_offset, bool(interleaved),
                       rope_scale)
     s, ctx = _launch(k, stream)
-    _check(_within(ctx, csa_cache_append, a, s), "csa_cache_append")
+    with ctx:
+        st = csa_cache_append(a, s)
+    if st:
+        raise L.CsaError(st, "csa_cache_append")
 
 
 def cache_read(cache: Cache, page_table, kv_len, T: int, *, out=None, stream=None):
@@ -368,16 +370,15 @@ def cache_read(cache: Cache, page_table, kv_len, T: int, *, out=None, stream=Non
     shape = (B, int(T), c.H, c.D)
     if out is not None and (out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous()):
         raise TypeError(f"out must be a contiguous bfloat16 tensor of shape {shape}")
-    _on(dev, cache=cache, page_table=page_table, kv_len=kv_len, out=out)
+    _on(dev, "cache.data cache.scale page_table kv_len out", cache.data, cache.scale, page_table, kv_len, out)
     s, ctx = _launch(cache.data, stream)
-
-    def call(out):
+    with ctx:
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=cache.data.device)
-        _check(csa_cache_read(CsaCacheReadArgs(c, *pages, B, shape[1], out.data_ptr()), s), "csa_cache_read")
-        return out
-
-    return _within(ctx, call, out)
+            out = cache.data.new_empty(shape, dtype=torch.bfloat16)
+        st = csa_cache_read(CsaCacheReadArgs(c, *pages, B, shape[1], out.data_ptr()), s)
+    if st:
+        raise L.CsaError(st, "csa_cache_read")
+    return out
 
 
 def cache_attention(q, cache_k: Cache, cache_v: Cache, page_table, kv_len, *, scale: float, idx=None,
@@ -399,24 +400,22 @@ def cache_attention(q, cache_k: Cache, cache_v: Cache, page_table, kv_len, *, sc
                                   ("lse", lse, torch.float32, (B, S, HA))):
         if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
             raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
-    _on(dev, q=q, cache_k=cache_k, cache_v=cache_v, page_table=page_table, kv_len=kv_len, idx=idx, out=out, lse=lse,
-        workspace=workspace)
+    _on(dev, "q cache_k.data cache_k.scale cache_v.data cache_v.scale page_table kv_len idx out lse workspace", q,
+        cache_k.data, cache_k.scale, cache_v.data, cache_v.scale, page_table, kv_len, idx, out, lse, workspace)
     s, ctx = _launch(q, stream)
-
-    def call(out, lse, workspace):
+    with ctx:
         if out is None:
-            out = torch.empty((B, S, HA, vc.D), dtype=torch.bfloat16, device=q.device)
+            out = torch.empty_like(q) if vc.D == kc.D else q.new_empty((B, S, HA, vc.D))
         if lse is None and return_lse:
-            lse = torch.empty((B, S, HA), dtype=torch.float32, device=q.device)
+            lse = q.new_empty((B, S, HA), dtype=torch.float32)
         a = CsaCacheAttnArgs(q.data_ptr(), kc, vc, *pages, ip, topk, B, S, HA, bool(causal), scale, out.data_ptr(),
-                             lse.data_ptr() if lse is not None else None)
+                             None if lse is None else lse.data_ptr())
         if workspace is None:
             size = csa_cache_attention_workspace_size(a)
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+            ws = q.new_empty(size, dtype=torch.uint8) if size else None
         else:
-            size = workspace.numel() * workspace.element_size()
-        _check(csa_cache_attention(a, workspace.data_ptr() if workspace is not None else None, size, s),
-               "csa_cache_attention")
-        return (out, lse) if return_lse else out
-
-    return _within(ctx, call, out, lse, workspace)
+            ws, size = workspace, workspace.numel() * workspace.element_size()
+        st = csa_cache_attention(a, None if ws is None else ws.data_ptr(), size, s)
+    if st:
+        raise L.CsaError(st, "csa_cache_attention")
+    return (out, lse) if return_lse else out

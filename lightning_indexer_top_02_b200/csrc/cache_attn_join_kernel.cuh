@@ -6,6 +6,12 @@
 namespace csa {
 namespace cattn {
 
+// Waits until the kernel launched before this one has ended and its results can be
+// read.  Every block does, before it returns too: what follows on the stream waits
+// for this kernel only.
+__device__ __forceinline__ void after_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+
 // Joins the pieces of the row tiles that several CTAs of the kernel above share: out =
 // sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.  A block takes rows of sequence
 // blockIdx.x, its warps every fourth piece of a row.
@@ -16,9 +22,10 @@ __global__ void __launch_bounds__(kThreads) cache_attn_pieces_kernel(const AttnP
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.x;
     const int all = chunks_of(p, b);
-    if (all == 0)
-        return;                                          // written by the kernel above
     const long long total = chunks_before(p, p.B, scratch), first = chunks_before(p, b, scratch);
+    after_kernel_before();
+    if (all == 0)
+        return;                                          // written by that kernel
     const int ctas = static_cast<int>(min(static_cast<long long>(p.ctas), total));
     for (int row = blockIdx.y; row < p.S * p.HA; row += gridDim.y) {
         const int i = row / p.HA, head = row - i * p.HA, h = head / p.G;
@@ -83,6 +90,7 @@ __global__ void __launch_bounds__(kThreads) cache_attn_pieces_kernel(const AttnP
 __global__ void __launch_bounds__(128) cache_attn_join_kernel(const AttnParams p, int Dv, int tile_rows,
                                                               long long rows)
 {
+    after_kernel_before();
     const int lane = threadIdx.x & 31;
     const long long at = blockIdx.x * 4ll + (threadIdx.x >> 5);   // (b, i, head)
     if (at >= rows)

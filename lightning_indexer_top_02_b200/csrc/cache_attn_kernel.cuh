@@ -298,6 +298,12 @@ struct Shape {
     static constexpr int kCtas = kNT == 1 && kDk + kDv <= 384 ? 3 : 2;
 };
 
+// The kernel that joins the pieces may take the SMs' free places from here on.
+__device__ __forceinline__ void next_kernel_may_begin()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Chunks of one row tile of sequence b.  (A tile of early queries sees less of the
 // sequence; the chunks past that find nothing to do.)
 __device__ __forceinline__ int chunks_of(const AttnParams &p, int b)
@@ -397,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
             *abort = 0;
     }
     __syncthreads();
+    next_kernel_may_begin();
     // the CTA's share: `left` chunks from chunk y of sequence `seq` on
     long long left = 1, y = 0;
     int seq = 0;

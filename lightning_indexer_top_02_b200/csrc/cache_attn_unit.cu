@@ -15,6 +15,8 @@ namespace {
 template <int kDk, int kDv>
 void cattn_pick(CattnPlan *pl)
 {
+    static std::atomic<unsigned long long> ready[6];
+    pl->ready = &ready[pl->wide ? 4 + (pl->tile_rows == kWideRows) : 2 * (pl->tile_rows > 8) + pl->bulk];
     if (pl->wide) {
         pl->keys = WideShape<kDk, kDv>::kKeys;
         pl->raw = 2 * kGatherWarps * WideShape<kDk, kDv>::kRaw;

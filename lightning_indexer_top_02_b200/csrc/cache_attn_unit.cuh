@@ -2,6 +2,8 @@
 // kernels (one for each key width: cache_attn_unit.cu) give the host code.  One
 // unit for all of them takes minutes to compile.
 #pragma once
+#include <atomic>
+
 #include "cache_attn_kernel.cuh"
 #include "cache_attn_wide_kernel.cuh"
 
@@ -25,6 +27,7 @@ struct CattnPlan {
     CattnFn fn;
     CattnWideFn wide_fn;
     int smem;
+    std::atomic<unsigned long long> *ready;  // devices that the kernel has been set up on, one bit each
 };
 
 // Fill in the kernel for keys of 64 .. 256 elements and values of dv; false: there is none.

@@ -811,6 +811,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_attn_wide_kernel(const 
     tc_fence_after();
     const uint32_t tmem = bars->tmem_addr;
     const WaitCtl ctl{&bars->abort, wp.wait_limit};
+    next_kernel_may_begin();
     if (warp < 4) {
         regs_inc<kWideSoftmaxRegs>();
         wide_softmax<kDk, kDv, kSplit>(wp, smem, bars, tmem, ctl);

@@ -97,6 +97,24 @@ bool same_pages(const csa_cache_t &a, const csa_cache_t &b)
     return a.dtype == b.dtype && a.H == b.H && a.num_pages == b.num_pages && a.page_size == b.page_size;
 }
 
+// Launches a kernel that may begin while the one before it on the stream ends; it waits
+// for that one's results itself (after_kernel_before).
+template <typename... P>
+void launch_behind(void (*fn)(P...), dim3 grid, int threads, cudaStream_t stream, P... args)
+{
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    (void)cudaLaunchKernelEx(&cfg, fn, args...);         // (launched() reports)
+}
+
 csa_status_t launched() { return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
 
 } // namespace
@@ -496,6 +514,25 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
     return CSA_OK;
 }
 
+// Whether a kernel's shared memory has been allowed for on the current device; done
+// once, by the most the kernel can ask for.
+bool is_ready(const CattnPlan &pl)
+{
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && dev < 64 && pl.ready->load(std::memory_order_acquire) >> dev & 1ull;
+}
+
+bool set_ready(const CattnPlan &pl, const void *fn)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.wide ? kSmemLimit : pl.smem) != cudaSuccess)
+        return false;
+    if (dev < 64)
+        pl.ready->fetch_or(1ull << dev, std::memory_order_release);
+    return true;
+}
+
 // The tiles' launch: the persistent tcgen05 kernel.
 csa_status_t launch_wide(const csa_cache_attn_args_t *a, const CattnPlan &pl, const csa::cattn::AttnParams &p,
                          cudaStream_t stream)
@@ -530,15 +567,19 @@ csa_status_t launch_wide(const csa_cache_attn_args_t *a, const CattnPlan &pl, co
     smem = smem < kSmemLimit / 2 + 1024 ? kSmemLimit / 2 + 1024 : smem;
     w.wait_limit = static_cast<long long>(g_wait_limit);
     const int sms = device_sms();
-    if (sms <= 0 || cudaFuncSetAttribute(pl.wide_fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    if (sms <= 0)
         return CSA_ERR_CUDA;
-    // the warpgroups trade registers (setmaxnreg): only valid for a build with
-    // exactly the launch count that the split assumes
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, pl.wide_fn) != cudaSuccess)
-        return CSA_ERR_CUDA;
-    if (fa.numRegs != kWideLaunchRegs)
-        return CSA_ERR_UNSUPPORTED;
+    if (!is_ready(pl)) {
+        // the warpgroups trade registers (setmaxnreg): only valid for a build with
+        // exactly the launch count that the split assumes
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, pl.wide_fn) != cudaSuccess)
+            return CSA_ERR_CUDA;
+        if (fa.numRegs != kWideLaunchRegs)
+            return CSA_ERR_UNSUPPORTED;
+        if (!set_ready(pl, reinterpret_cast<const void *>(pl.wide_fn)))
+            return CSA_ERR_CUDA;
+    }
     pl.wide_fn<<<w.items < sms ? w.items : sms, kWideThreads, smem, stream>>>(w);
     return launched();
 }
@@ -614,7 +655,7 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
         st = CSA_ERR_CUDA;
     } else if (pl.wide) {
         st = launch_wide(a, pl, p, stream);
-    } else if (cudaFuncSetAttribute(pl.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem) != cudaSuccess) {
+    } else if (!is_ready(pl) && !set_ready(pl, reinterpret_cast<const void *>(pl.fn))) {
         st = CSA_ERR_CUDA;
     } else {
         pl.fn<<<static_cast<unsigned>(pl.ctas ? pl.ctas : pl.works), csa::cattn::kThreads, pl.smem, stream>>>(p);
@@ -626,14 +667,14 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     const bool join = pl.wide ? pl.splits > 1 : pl.ctas > 0;
     if (st == CSA_OK && join) {
         if (pl.wide) {
-            csa::cattn::cache_attn_join_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(
-                p, a->cache_v.D, pl.tile_rows, rows);
+            launch_behind(csa::cattn::cache_attn_join_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, stream, p,
+                          a->cache_v.D, pl.tile_rows, rows);
         } else {
             // a block for every row, or several rows a block when there are many
             const int per = a->S * a->HA, most = 32 * device_sms() / a->B;
             const dim3 grid(a->B, per < most ? per : most < 1 ? 1 : most);
-            csa::cattn::cache_attn_pieces_kernel<<<grid, csa::cattn::kThreads, 0, stream>>>(p, a->cache_v.D,
-                                                                                           pl.tile_rows);
+            launch_behind(csa::cattn::cache_attn_pieces_kernel, grid, csa::cattn::kThreads, stream, p, a->cache_v.D,
+                          pl.tile_rows);
         }
         st = launched();
         if (st == CSA_OK && !mark(2, stream))
