@@ -117,8 +117,8 @@ csa_status_t csa_rotary(const csa_rotary_args_t *args, cudaStream_t stream);
  * by the token's position in the cache when positions is NULL; values are
  * not.  A rotated element is rounded once to fp32 (the products are carried
  * in more than 32 bits, so that a stored code does not depend on the order of
- * operations) and then to the cache's type.  Both caches have the same
- * num_pages, page_size, H and dtype.  Rows that no token goes to are left as they were.
+ * operations) and then to the cache's type.  The two caches are different memory
+ * with the same num_pages, page_size, H and dtype.  Rows that no token goes to are left as they were.
  */
 typedef struct {
     const void *k;               /* bf16 [N, H, Dk] at the strides below, 16-byte aligned */
@@ -168,9 +168,11 @@ csa_status_t csa_cache_read(const csa_cache_read_args_t *args, cudaStream_t stre
  * are exact in the tensor cores' 16-bit types; q.k and P.V accumulate in fp32, softmax
  * is fp32, the probabilities are rounded to 16 bits for P.V, out to bf16.
  * D of each cache is 64, 128, 192 or 256; HA a multiple of H, HA / H <= 128;
- * the caches have the same H, num_pages and page_size.
+ * the caches have the same H, num_pages and page_size, and may be the same one
+ * (values that are the keys).  out must not overlap q.
  * `workspace` is device memory of csa_cache_attention_workspace_size(args)
- * bytes (shapes and the device's SM count decide it, not the data), 256-byte
+ * bytes (shapes and the device's SM count decide it, not the data; 0 for arguments
+ * that the call rejects, or when it needs none), 256-byte
  * aligned, used by the enqueued work only and with no state to keep; NULL
  * allocates and frees it stream-ordered.  Calls that may overlap, replays of captured
  * graphs among them, need workspaces of their own.

@@ -395,6 +395,8 @@ def cache_attention(q, cache_k: Cache, cache_v: Cache, page_table, kv_len, *, sc
     if q.dtype != torch.bfloat16 or q.dim() != 4 or q.shape[0] != B or not q.is_contiguous() or q.shape[-1] != kc.D:
         raise TypeError("q must be a contiguous bfloat16 tensor [B, S, HA, Dk]")
     _, S, HA, _ = q.shape
+    if idx is not None and idx.numel() == 0 and B * S:
+        raise ValueError("idx has no entries (leave it out for every visible position)")
     ip, topk = (None, 0) if idx is None else (_int32("idx", idx, (B, S, idx.shape[-1])), idx.shape[-1])
     for name, t, dtype, shape in (("out", out, torch.bfloat16, (B, S, HA, vc.D)),
                                   ("lse", lse, torch.float32, (B, S, HA))):

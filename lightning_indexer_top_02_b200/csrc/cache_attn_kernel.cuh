@@ -435,6 +435,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
         int work = blockIdx.x, lo = 0, hi = 1, all = 1;      // the segment: chunks lo .. hi - 1 of `all`
         if (p.ctas) {
             all = chunks_of(p, seq);
+            if (all <= 0)
+                break;                                   // (the lengths changed meanwhile: not allowed, but no endless loop)
             const int w = static_cast<int>(y / all);
             lo = static_cast<int>(y - static_cast<long long>(w) * all);
             hi = static_cast<int>(min(static_cast<long long>(all), lo + left));

@@ -15,7 +15,7 @@ using csa::cache::CacheView;
 using csa::cache::FastDiv;
 using csa::cache::PageMap;
 
-constexpr long long kIntLimit = (1ll << 31) - 64;
+constexpr long long kIntLimit = (1ll << 31) - 1024;   // positions and rows, and a tile more, are ints
 
 // Bytes of a row's data and of its scales.
 long long cache_row_bytes(const csa_cache_t &c)
@@ -304,7 +304,7 @@ extern "C" csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStre
         st = validate_cache(a->cache_v);
     if (st != CSA_OK)
         return st;
-    if (a->v && !same_pages(a->cache_k, a->cache_v))
+    if (a->v && (!same_pages(a->cache_k, a->cache_v) || a->cache_k.data == a->cache_v.data))
         return CSA_ERR_INVALID_ARG;
     if (a->inv_freq && (a->rot_dim < 2 || a->rot_dim % 2 != 0 || a->rot_offset < 0 || a->rot_offset % 2 != 0 ||
                         a->rot_offset > a->cache_k.D - a->rot_dim || !std::isfinite(a->rope_scale) ||
@@ -454,7 +454,7 @@ csa_status_t validate_cattn(const csa_cache_attn_args_t *a)
     st = validate_pages(a->kv_len, a->page_table, a->max_pages, a->table_stride, a->cache_k.page_size);
     if (st != CSA_OK)
         return st;
-    if (!a->q || !a->out || !aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->idx, 4) ||
+    if (!a->q || !a->out || a->q == a->out || !aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->idx, 4) ||
         !aligned(a->lse, 4))
         return CSA_ERR_INVALID_ARG;
     if (static_cast<long long>(a->S) * a->HA >= kIntLimit || (a->idx && a->topk >= kIntLimit) ||

@@ -619,24 +619,19 @@ csa_status_t csa_last_device_error(cudaStream_t stream)
     int h[4] = {0, 0, 0, 0};
     if (cudaMemcpyFromSymbol(h, csa::g_csa_error, sizeof h) != cudaSuccess)
         return CSA_ERR_CUDA;
-    if (h[0] == 0) {
-        // the units that hold the cache attention kernels have words of their own
-        using namespace csa::cattn;
-        for (auto unit : {error_64, error_128, error_192, error_256}) {
-            int u[4] = {0, 0, 0, 0};
-            if (!unit(u))
-                return CSA_ERR_CUDA;
-            if (h[0] == 0)
-                h[0] = u[0];
-        }
-        if (h[0] == 0)
-            return CSA_OK;
-        return h[0] == csa::kErrTimeout ? CSA_ERR_TIMEOUT
-                                        : h[0] == csa::kErrDebugCheck ? CSA_ERR_DEBUG_CHECK : CSA_ERR_CUDA;
-    }
     const int zero[4] = {0, 0, 0, 0};
-    if (cudaMemcpyToSymbol(csa::g_csa_error, zero, sizeof zero) != cudaSuccess)
+    if (h[0] != 0 && cudaMemcpyToSymbol(csa::g_csa_error, zero, sizeof zero) != cudaSuccess)
         return CSA_ERR_CUDA;
+    // the units that hold the cache attention kernels have words of their own
+    using namespace csa::cattn;
+    for (auto unit : {error_64, error_128, error_192, error_256}) {
+        int u[4] = {0, 0, 0, 0};
+        if (!unit(u))
+            return CSA_ERR_CUDA;
+        h[0] = h[0] ? h[0] : u[0];
+    }
+    if (h[0] == 0)
+        return CSA_OK;
     if (h[0] == csa::kErrTimeout)
         return CSA_ERR_TIMEOUT;
     return h[0] == csa::kErrDebugCheck ? CSA_ERR_DEBUG_CHECK : CSA_ERR_CUDA;

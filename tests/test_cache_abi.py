@@ -25,7 +25,8 @@ def good_cache(dtype=C.CSA_CACHE_E2M1, D=128, H=2):
 
 def good_attn():
     a = C.CsaCacheAttnArgs()
-    a.q = a.out = a.kv_len = a.page_table = 4096
+    a.q = a.kv_len = a.page_table = 4096
+    a.out = 8192
     a.cache_k, a.cache_v = good_cache(), good_cache()
     a.max_pages = a.table_stride = 4
     a.B, a.S, a.HA, a.causal, a.scale = 0, 1, 8, 1, 0.1       # B = 0: valid, and launches nothing
@@ -79,7 +80,7 @@ def test_attention_refuses(field, value, status):
     assert L.csa_cache_attention_workspace_size(a) == 0
 
 
-@pytest.mark.parametrize("field,value,status", [("q", 0, 1), ("q", 4104, 1), ("out", 0, 1), ("out", 4104, 1), ("kv_len", 0, 1),
+@pytest.mark.parametrize("field,value,status", [("q", 0, 1), ("q", 4104, 1), ("q", 8192, 1), ("out", 0, 1), ("out", 4104, 1), ("kv_len", 0, 1),
                                                 ("page_table", 0, 1), ("page_table", 4098, 1), ("max_pages", 0, 1),
                                                 ("table_stride", 3, 1), ("max_pages", 1 << 28, 1), ("idx", 4098, 1),
                                                 ("lse", 4098, 1)])
@@ -118,12 +119,13 @@ def test_append_refuses(field, value, status):
 
 @pytest.mark.parametrize("field,value", [("k", 0), ("k", 4104), ("v", 4104), ("kv_len", 0), ("page_table", 0), ("k_token_stride", 4),
                                          ("k_head_stride", -8), ("v_token_stride", 4), ("cu_tokens", 4098), ("positions", 4098),
-                                         ("table_stride", 0), ("max_pages", 0)])
+                                         ("table_stride", 0), ("max_pages", 0), ("cache_v.data", 4096)])
 def test_append_refuses_pointers(field, value):
     a = good_append()
     a.S, a.N = 1, 2
     a.v, a.cache_v, a.v_token_stride, a.v_head_stride = 4096, good_cache(), 256, 128
-    setattr(a, field, value)
+    a.cache_v.data = 8192
+    set_path(a, field, value)
     assert L.csa_cache_append(a, None) == L.CSA_ERR_INVALID_ARG
 
 

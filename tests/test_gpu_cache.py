@@ -454,6 +454,67 @@ def test_workspace(lib):
     assert torch.equal(out, want)
 
 
+def test_attention_empty_selection(lib):
+    """An empty list is not "every position"."""
+    L, g = lib, gen(4)
+    c = random_cache(L, "e2m1", 4, 16, 1, 128, g)
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+    q = torch.zeros((1, 1, 8, 128), dtype=torch.bfloat16, device="cuda")
+    lens = torch.ones(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        L.cache_attention(q, c, c, table, lens, scale=1.0, idx=torch.zeros((1, 1, 0), dtype=torch.int32, device="cuda"))
+    with pytest.raises(L.CsaError):                        # in place: q is read while out is written
+        L.cache_attention(q, c, c, table, lens, scale=1.0, out=q)
+    none = L.cache_attention(q[:0], c, c, table[:0], lens[:0], scale=1.0, return_lse=True)
+    assert none[0].shape == (0, 1, 8, 128) and none[1].shape == (0, 1, 8)
+
+
+@pytest.mark.parametrize("HA,page", [(64, 64), (128, 24)])
+def test_attention_wait_limit(lib, HA, page):
+    """A wait that runs out ends the call with an error status, and the next call is right.  (Up to 16 rows a
+    copy from L2 has often landed before it is first waited for.)"""
+    L, g = lib, gen(HA)
+    c = random_cache(L, "e2m1", 200, page, 1, 128, g)
+    table = torch.arange(200, dtype=torch.int32, device="cuda").view(1, 200)
+    q = torch.randn((1, 1, HA, 128), generator=g, device="cuda").to(torch.bfloat16)
+    lens = torch.tensor([4000], dtype=torch.int32, device="cuda")
+    want = L.cache_attention(q, c, c, table, lens, scale=0.09)
+    no_device_error(L)
+    L.csa_set_wait_limit(1)
+    try:
+        L.cache_attention(q, c, c, table, lens, scale=0.09)
+        assert L.csa_last_device_error(None) == L.CSA_ERR_TIMEOUT
+    finally:
+        L.csa_set_wait_limit(0)
+    assert torch.equal(L.cache_attention(q, c, c, table, lens, scale=0.09), want)
+    no_device_error(L)
+
+
+def test_attention_ragged_batches(lib):
+    """Many sequences of very different lengths: shares that begin and end anywhere, whole tiles, unused places."""
+    lens = [0, 1, 3000, 17, 0, 255, 256, 257, 1024, 5, 0, 0, 700] * 12        # more sequences than threads in a block
+    for HA, H, S in ((8, 2, 1), (16, 1, 1), (4, 4, 3)):
+        check_attention(lib, B=len(lens), S=S, HA=HA, H=H, Dk=64, Dv=64, page=32, lens=lens, seed=HA + S)
+
+
+def test_calls_at_once(lib):
+    """Two streams at a time, each with what it allocates itself."""
+    L = lib
+    states = [step_state(L, T=200), step_state(L, T=200)]
+    want = [L.cache_attention(s["q"], s["kc"], s["vc"], s["table"], s["lens"], scale=0.09) for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    got = [[], []]
+    for _ in range(20):
+        for i, (s, st) in enumerate(zip(states, streams)):
+            got[i].append(L.cache_attention(s["q"], s["kc"], s["vc"], s["table"], s["lens"], scale=0.09, stream=st))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for x in g:
+            assert torch.equal(x, w)
+    no_device_error(L)
+
+
 # ---------------------------------------------------------------- together
 
 def decode_step(L, s, stream=None):
