@@ -145,6 +145,32 @@ __device__ __forceinline__ float2 float2_of_bf16x2(uint32_t w)
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// 32 bytes a lane at once where they stand on 32 bytes (a whole sector: two stores of
+// 16 at a stride of 32 each write half of every sector they touch).
+__device__ __forceinline__ void store32(uint8_t *dst, const uint4 &a, const uint4 &b)
+{
+    if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y), "r"(a.z),
+                     "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = a;
+        reinterpret_cast<uint4 *>(dst)[1] = b;
+    }
+}
+
+__device__ __forceinline__ void load32(const void *src, uint4 &a, uint4 &b)
+{
+    if ((reinterpret_cast<uintptr_t>(src) & 31) == 0) {
+        asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+            : "l"(src));
+    } else {
+        a = __ldg(static_cast<const uint4 *>(src));
+        b = __ldg(static_cast<const uint4 *>(src) + 1);
+    }
+}
+
 // The angle pos * freq as a fraction of half turns in [-1, 1], reduced in
 // double: the product is exact (31 + 24 bits), 1 / 2 pi costs one rounding, so
 // the reduced angle is good to 2^-52 of the turns taken, at any position.

@@ -414,7 +414,7 @@ extern "C" csa_status_t csa_cache_read(const csa_cache_read_args_t *args, cudaSt
     p.out = static_cast<__nv_bfloat16 *>(a->out);
     const int per = csa::cache::kRowThreads / p.lanes * csa::cache::kReadAhead;
     const unsigned rows_y = a->B < 65535 ? a->B : 65535;
-    long long need = (static_cast<long long>(p.rows) + per - 1) / per, most = (64ll * sms + rows_y - 1) / rows_y;
+    long long need = (static_cast<long long>(p.rows) + per - 1) / per, most = (16ll * sms + rows_y - 1) / rows_y;
     const dim3 grid(static_cast<unsigned>(need < most ? need : most), rows_y);
     if (!mark(0, stream))
         return CSA_ERR_CUDA;

@@ -70,11 +70,7 @@ __device__ __forceinline__ float turned(float a, float ch, float cl, float b, fl
 // 16 consecutive bf16 elements.
 struct Raw16 {
     uint4 a, b;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *src)
-    {
-        a = __ldg(reinterpret_cast<const uint4 *>(src));
-        b = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
-    }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *src) { load32(src, a, b); }
     __device__ __forceinline__ void unpack(float (&x)[16]) const
     {
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -106,9 +102,7 @@ __device__ __forceinline__ void store16(const CacheView &c, uint8_t *data, uint8
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 u[j] = bf16x2_of(x[2 * j], x[2 * j + 1]);
-            uint4 *dst = reinterpret_cast<uint4 *>(data + 32 * lane);
-            dst[0] = w[0];
-            dst[1] = w[1];
+            store32(data + 32 * lane, w[0], w[1]);
         }
     } else if constexpr (kType == 1) {
         if (!active)
@@ -245,6 +239,11 @@ struct RowWalk {
         uint8_t *data = nullptr, *scale = nullptr;
         const int pg = page[r.tok];
         const bool active = r.head >= 0 && pg >= 0;
+        if constexpr (kType == 0 && kHow == kStill) {   // bf16 to bf16
+            if (active)
+                store32(const_cast<uint8_t *>(row_data(c, p.pm, pg, r.head, off[r.tok])) + 32 * lane, r.own.a, r.own.b);
+            return;
+        }
         if (active) {
             r.own.unpack(x);
             rotate16<kHow>(row(r), 16 * lane, p.off, p.half, turns + r.tok * turn_at(p.half), r.other, x);
@@ -350,8 +349,7 @@ struct Held16 {
     __device__ __forceinline__ void load(const uint8_t *data, const uint8_t *scale, int lane)
     {
         if constexpr (kType == 0) {
-            a = __ldg(reinterpret_cast<const uint4 *>(data) + 2 * lane);
-            b = __ldg(reinterpret_cast<const uint4 *>(data) + 2 * lane + 1);
+            load32(data + 32 * lane, a, b);
         } else if constexpr (kType == 1) {
             a = __ldg(reinterpret_cast<const uint4 *>(data) + lane);
             s = __ldg(reinterpret_cast<const float *>(scale));
@@ -363,7 +361,7 @@ struct Held16 {
         }
     }
 
-    __device__ __forceinline__ void store(uint4 *dst, float tensor_scale) const
+    __device__ __forceinline__ void store(uint8_t *dst, float tensor_scale) const
     {
         uint4 w[2];
         uint32_t *u = reinterpret_cast<uint32_t *>(w);
@@ -394,8 +392,7 @@ struct Held16 {
                 u[4 * j + 3] = bf16x2_of(f3.x * f, f3.y * f);
             }
         }
-        dst[0] = w[0];
-        dst[1] = w[1];
+        store32(dst, w[0], w[1]);
     }
 };
 
@@ -412,21 +409,23 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p)
     for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
         const int len = __ldg(p.kv_len + b);
         const int32_t *table = p.pm.table + b * p.pm.table_stride;
-        uint4 *out = reinterpret_cast<uint4 *>(p.out + static_cast<long long>(b) * p.rows * p.D);
-        const unsigned stride = gridDim.x * per;
-        for (unsigned r0 = blockIdx.x * per * kReadAhead + threadIdx.x / p.lanes; r0 < p.rows;
-             r0 += stride * kReadAhead) {
-            int t[kReadAhead], page[kReadAhead];
-            bool has[kReadAhead];
+        uint8_t *out = reinterpret_cast<uint8_t *>(p.out + static_cast<long long>(b) * p.rows * p.D);
+        const unsigned stride = gridDim.x * per * kReadAhead;
+        int t[kReadAhead], page[kReadAhead];             // of the rows worked on next
+        auto find = [&](unsigned r0) {
 #pragma unroll
             for (int k = 0; k < kReadAhead; ++k) {
                 const unsigned r = r0 + k * per;
                 t[k] = static_cast<int>(p.div_H.div(min(r, static_cast<unsigned>(p.rows - 1))));
                 const int n = static_cast<int>(p.pm.div.div(t[k]));
-                has[k] = r < p.rows && t[k] < len && n < p.pm.max_pages;
-                page[k] = has[k] ? __ldg(table + n) : -1;
+                page[k] = r < p.rows && t[k] < len && n < p.pm.max_pages ? __ldg(table + n) : -1;
             }
+        };
+        unsigned r0 = blockIdx.x * per * kReadAhead + threadIdx.x / p.lanes;
+        find(r0);
+        for (; r0 < p.rows; r0 += stride) {
             Held16<kType> x[kReadAhead];
+            bool has[kReadAhead];
 #pragma unroll
             for (int k = 0; k < kReadAhead; ++k) {
                 has[k] = page[k] >= 0 && page[k] < p.pm.num_pages;
@@ -435,18 +434,17 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p)
                 if (has[k])
                     x[k].load(row_data(p.c, p.pm, page[k], h, off), row_scale(p.c, p.pm, page[k], h, off), lane);
             }
+            find(r0 + stride);                           // (the next rows' pages come meanwhile)
 #pragma unroll
             for (int k = 0; k < kReadAhead; ++k) {
                 const unsigned r = r0 + k * per;
                 if (r >= p.rows)
                     break;
-                uint4 *dst = out + (static_cast<long long>(r) * p.D + 16 * lane) / 8;
-                if (has[k]) {
+                uint8_t *dst = out + (static_cast<long long>(r) * p.D + 16 * lane) * 2;
+                if (has[k])
                     x[k].store(dst, p.c.tensor_scale);
-                } else {
-                    dst[0] = make_uint4(0u, 0u, 0u, 0u);
-                    dst[1] = make_uint4(0u, 0u, 0u, 0u);
-                }
+                else
+                    store32(dst, make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u));
             }
         }
     }
