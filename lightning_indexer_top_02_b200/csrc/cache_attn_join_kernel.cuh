@@ -35,14 +35,11 @@ __global__ void __launch_bounds__(kThreads) cache_attn_pieces_kernel(const AttnP
         const int k0 = cta_of(start, total, ctas), k1 = cta_of(start + all - 1, total, ctas);
         if (k0 == k1)
             continue;                                    // one CTA had the whole tile
-        const long long stride = static_cast<long long>(tile_rows) * (Dv + 2);
         // the first CTA's piece begins the tile (its second slot), the others' end or fill it
-        auto piece = [&](int k) {
-            return p.part + (2ll * k + (k == k0 ? 1 : 0)) * stride + (r % tile_rows) * (Dv + 2);
-        };
+        auto piece = [&](int k) { return (2ll * k + (k == k0 ? 1 : 0)) * tile_rows + r % tile_rows; };
         float top = -INFINITY;
         for (int k = k0 + threadIdx.x; k <= k1; k += kThreads)
-            top = fmaxf(top, piece(k)[Dv]);
+            top = fmaxf(top, p.stat[piece(k)].x);
 #pragma unroll
         for (int d = 16; d; d >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -55,9 +52,10 @@ __global__ void __launch_bounds__(kThreads) cache_attn_pieces_kernel(const AttnP
         float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
 #pragma unroll 4
         for (int k = k0 + warp; k <= k1; k += kWarps) {
-            const float *src = piece(k);
-            const float a = ex2_approx(src[Dv] - base);
-            sum += a * src[Dv + 1];
+            const float *src = p.part + piece(k) * Dv;
+            const float2 st = p.stat[piece(k)];
+            const float a = ex2_approx(st.x - base);
+            sum += a * st.y;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (64 * j < Dv) {
@@ -101,33 +99,35 @@ __global__ void __launch_bounds__(128) cache_attn_join_kernel(const AttnParams p
     const int r = p.idx ? head - h * p.G : static_cast<int>(bi % p.S) * p.G + head - h * p.G;
     const long long group = p.idx ? bi * p.H + h : bi / p.S * p.H + h;
     const long long work = group * p.tiles + r / tile_rows;
-    const long long stride = static_cast<long long>(tile_rows) * (Dv + 2);
-    const float *src = p.part + work * p.splits * stride + (r % tile_rows) * (Dv + 2);
+    const long long first = work * p.splits * tile_rows + r % tile_rows;
     float top = -INFINITY;
     for (int s = lane; s < p.splits; s += 32)
-        top = fmaxf(top, src[s * stride + Dv]);
+        top = fmaxf(top, p.stat[first + static_cast<long long>(s) * tile_rows].x);
 #pragma unroll
     for (int d = 16; d; d >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    float sum = 0.0f;
-    if (top != -INFINITY)
-        for (int s = lane; s < p.splits; s += 32)
-            sum += ex2_approx(src[s * stride + Dv] - top) * src[s * stride + Dv + 1];
+    const float base = top == -INFINITY ? 0.0f : top;
+    float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+        const long long piece = first + static_cast<long long>(s) * tile_rows;
+        const float2 st = p.stat[piece];
+        const float a = ex2_approx(st.x - base);
+        sum += a * st.y;
 #pragma unroll
-    for (int d = 16; d; d >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
-    for (int d = 2 * lane; d < Dv; d += 64) {
-        float x = 0.0f, y = 0.0f;
-        if (top != -INFINITY)
-            for (int s = 0; s < p.splits; ++s) {
-                const float a = ex2_approx(src[s * stride + Dv] - top);
-                const float2 v = *reinterpret_cast<const float2 *>(src + s * stride + d);
-                x += a * v.x;
-                y += a * v.y;
+        for (int j = 0; j < 4; ++j)
+            if (64 * j < Dv) {
+                const float2 v = *reinterpret_cast<const float2 *>(p.part + piece * Dv + 64 * j + 2 * lane);
+                x[2 * j] += a * v.x;
+                x[2 * j + 1] += a * v.y;
             }
-        *reinterpret_cast<uint32_t *>(p.out + at * Dv + d) = cache::bf16x2_of(x * inv, y * inv);
     }
+    const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (64 * j < Dv)
+            *reinterpret_cast<uint32_t *>(p.out + at * Dv + 64 * j + 2 * lane) =
+                cache::bf16x2_of(x[2 * j] * inv, x[2 * j + 1] * inv);
     if (p.lse && lane == 0)
         p.lse[at] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }

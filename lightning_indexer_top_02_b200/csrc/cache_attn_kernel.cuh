@@ -83,7 +83,8 @@ struct AttnParams {
     int tiles;                              // row tiles of a group
     int rows;                               // query rows of a group: S * G, or G with idx
     int capacity;                           // positions the page table reaches
-    float *part;                            // [piece][rows of a tile][Dv + 2]
+    float *part;                            // [piece][rows of a tile][Dv]: O before it is divided
+    float2 *stat;                           // [piece][rows of a tile]: its maximum (log2) and sum
     FastDiv div_splits, div_tiles, div_H, div_S, div_G;
 };
 
@@ -863,7 +864,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
             }
             if (hi - lo < all) {
                 // a piece: the CTA's first one ends a tile that another began, or it begins one
-                float *dst = p.part + (static_cast<long long>(2 * blockIdx.x + (lo > 0 ? 0 : 1)) * RT + r) * (kDv + 2);
+                const long long piece = static_cast<long long>(2 * blockIdx.x + (lo > 0 ? 0 : 1)) * RT + r;
+                float *dst = p.part + piece * kDv;
                 for (int d = lane; d < kDv; d += 32) {
                     float x = 0.0f;
 #pragma unroll
@@ -871,10 +873,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
                         x += a[w] * row[w * RT * (kDv + 2) + d];
                     dst[d] = x;
                 }
-                if (lane == 0) {
-                    dst[kDv] = top;
-                    dst[kDv + 1] = sum;
-                }
+                if (lane == 0)
+                    p.stat[piece] = make_float2(top, sum);
                 continue;
             }
             int i, head;

@@ -20,7 +20,7 @@ struct CattnPlan {
     bool bulk;              // tiles of 16 keys lie together in a page (the register kernel)
     int keys, raw;          // of the wide kernel: keys of a tile, staging bytes
     int tile_rows, tiles, rows, splits;
-    long long works;
+    long long works, piece_rows;
     size_t workspace;
     int chunk;              // keys that are shared out together
     int ctas;               // of the register kernel: those that share the chunks, 0: one a row tile

@@ -95,6 +95,16 @@ struct WideBarriers {
     int abort;
 };
 
+// Every thread calls this once, when it has started what needs neither barriers nor
+// TMEM (the first loads): the barriers are there from here on.  Returns TMEM's address.
+__device__ __forceinline__ uint32_t wide_ready(const WideBarriers *bars)
+{
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return bars->tmem_addr;
+}
+
 // What every role needs to know of an item.
 struct Item {
     Group g;
@@ -262,6 +272,7 @@ __device__ void wide_gather(const WideParams &wp, uint8_t *smem, WideBarriers *b
     bool have = start(0), ok = true;
     fetch_page();
     fetch_pos();
+    wide_ready(bars);
     Ring kr, vr;
     for (int gt = 0; have; ++gt) {
         const bool next = start(gt + 1);
@@ -485,8 +496,7 @@ struct WideRow {
 };
 
 template <int kDk, int kDv, bool kSplit>
-__device__ void wide_softmax(const WideParams &wp, uint8_t *smem, WideBarriers *bars, uint32_t tmem,
-                             const WaitCtl &ctl)
+__device__ void wide_softmax(const WideParams &wp, uint8_t *smem, WideBarriers *bars, const WaitCtl &ctl)
 {
     constexpr int kTileRows = kSplit ? kWideRows / 2 : kWideRows;
     using Sh = WideShape<kDk, kDv>;
@@ -497,7 +507,7 @@ __device__ void wide_softmax(const WideParams &wp, uint8_t *smem, WideBarriers *
     const int quarter = kSplit ? warp & 1 : warp;
     const int half = kSplit ? warp >> 1 : 0;
     const int row = 32 * quarter + lane;                      // of the tile
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;  // the warp's TMEM lanes
     Ring sr;
     float *xo = reinterpret_cast<float *>(smem + wp.off_x);   // kSplit: [warp][kXCols columns][32 lanes]
     int gt = 0, xc = 0;
@@ -554,6 +564,7 @@ __device__ void wide_softmax(const WideParams &wp, uint8_t *smem, WideBarriers *
         }
     };
     WideRow cur = look(blockIdx.x);
+    lanes += wide_ready(bars);
     begin(cur);
     while (cur.item < wp.items && ok) {
         float m = -INFINITY, l = 0.0f;
@@ -689,23 +700,29 @@ __device__ void wide_softmax(const WideParams &wp, uint8_t *smem, WideBarriers *
         }
         const bool part = p.splits > 1;
         const float norm = part ? 1.0f : (l > 0.0f ? p.v_scale / l : 0.0f);
-        float *dst = part ? p.part + (static_cast<long long>(cur.item) * kTileRows + row) * (kDv + 2) : nullptr;
+        const long long piece = static_cast<long long>(cur.item) * kTileRows + row;
+        float *dst = p.part + piece * kDv;
         __nv_bfloat16 *out = p.out + at * kDv;
         auto put = [&](int c, const float (&x)[kXCols]) {
             if (!real)
                 return;
             if (part) {
 #pragma unroll
-                for (int j = 0; j < kXCols; j += 2)
-                    *reinterpret_cast<float2 *>(dst + c + j) = make_float2(x[j], x[j + 1]);
+                for (int j = 0; j < kXCols; j += 8) {
+                    const uint32_t *u = reinterpret_cast<const uint32_t *>(x + j);
+                    cache::store32(reinterpret_cast<uint8_t *>(dst + c + j), make_uint4(u[0], u[1], u[2], u[3]),
+                                   make_uint4(u[4], u[5], u[6], u[7]));
+                }
             } else {
 #pragma unroll
-                for (int j = 0; j < kXCols; j += 8)
-                    *reinterpret_cast<uint4 *>(out + c + j) =
-                        make_uint4(cache::bf16x2_of(x[j] * norm, x[j + 1] * norm),
-                                   cache::bf16x2_of(x[j + 2] * norm, x[j + 3] * norm),
-                                   cache::bf16x2_of(x[j + 4] * norm, x[j + 5] * norm),
-                                   cache::bf16x2_of(x[j + 6] * norm, x[j + 7] * norm));
+                for (int j = 0; j < kXCols; j += 16) {
+                    uint32_t u[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        u[e] = cache::bf16x2_of(x[j + 2 * e] * norm, x[j + 2 * e + 1] * norm);
+                    cache::store32(reinterpret_cast<uint8_t *>(out + c + j), make_uint4(u[0], u[1], u[2], u[3]),
+                                   make_uint4(u[4], u[5], u[6], u[7]));
+                }
             }
         };
         auto take = [&](int c, float (&x)[kXCols]) {           // O's columns c.., scaled
@@ -753,8 +770,7 @@ __device__ void wide_softmax(const WideParams &wp, uint8_t *smem, WideBarriers *
         }
         if (real && half == 0) {
             if (part) {
-                dst[kDv] = m;
-                dst[kDv + 1] = l;
+                p.stat[piece] = make_float2(m, l);
             } else if (p.lse) {
                 p.lse[at] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
             }
@@ -806,20 +822,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_attn_wide_kernel(const 
         tmem_alloc(&bars->tmem_addr, 512);
         tmem_relinquish();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = bars->tmem_addr;
     const WaitCtl ctl{&bars->abort, wp.wait_limit};
     next_kernel_may_begin();
+    uint32_t tmem = 0;
     if (warp < 4) {
         regs_inc<kWideSoftmaxRegs>();
-        wide_softmax<kDk, kDv, kSplit>(wp, smem, bars, tmem, ctl);
+        wide_softmax<kDk, kDv, kSplit>(wp, smem, bars, ctl);
     } else if (warp < kWideMmaWarp) {
         regs_dec<kWideGatherRegs>();
         wide_gather<kDk, kDv>(wp, smem, bars, ctl, kTileRows);
     } else {
         regs_dec<kWideMmaRegs>();
+        tmem = wide_ready(bars);
         if (warp == kWideMmaWarp && lane == 0)
             wide_mma<kDk, kDv>(wp, smem, bars, tmem, ctl, kTileRows);
     }

@@ -510,7 +510,8 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
     if (pl->works * pl->splits >= kIntLimit)
         return CSA_ERR_UNSUPPORTED;
     const long long pieces = pl->wide ? (pl->splits > 1 ? pl->works * pl->splits : 0) : 2ll * pl->ctas;
-    pl->workspace = static_cast<size_t>(pieces) * pl->tile_rows * (a->cache_v.D + 2) * sizeof(float);
+    pl->piece_rows = pieces * pl->tile_rows;
+    pl->workspace = static_cast<size_t>(pl->piece_rows) * (a->cache_v.D + 2) * sizeof(float);
     return CSA_OK;
 }
 
@@ -651,6 +652,7 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     p.div_S = FastDiv::of(p.S);
     p.div_G = FastDiv::of(p.G);
     p.part = static_cast<float *>(ws);
+    p.stat = reinterpret_cast<float2 *>(p.part + pl.piece_rows * a->cache_v.D);
     if (!mark(0, stream)) {
         st = CSA_ERR_CUDA;
     } else if (pl.wide) {
