@@ -40,6 +40,12 @@
 // copy each; else every row is found by itself and copied 16 bytes at a time, which
 // takes about 150 instructions more of some 750 a block.
 //
+// Measured at 32 sequences of 512 .. 32,768 keys, 64 heads over 8, D = 128 (615 MB of
+// cache): 151 us, 4.1 TB/s.  Memory alone (the arithmetic left out) takes 111 us, the
+// arithmetic alone 115: 617 instructions for 32 keys, of which 256 are the conversions
+// (64 + 64 of codes, 64 + 64 multiplications by scales, both on half-rate pipes).  12 warps an
+// SM; 8 or 16 warps, deeper staging or shorter blocks were slower (150 -> 158 .. 188 us).
+//
 // The CTAs that the GPU holds share out all the chunks (256 or 128 keys) of all row tiles,
 // evenly and in order, whatever the sequences' lengths: a CTA's share is a run of
 // chunks, which ends one tile, takes whole ones and begins another.  In a tile the
