@@ -133,14 +133,14 @@ def make_cache(dtype: str, num_pages: int, page_size: int, H: int, D: int, *, de
                  torch.zeros(shape + (D // 16,), dtype=torch.uint8, device=device), tensor_scale)
 
 
-def _page_stride(name, t):
+def _page_stride(t):
     """Bytes from page to page of a tensor that is dense within a page (0: dense altogether)."""
     if t.is_contiguous():
         return 0
     n = 1
     for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if size != 1 and stride != n:
-            raise ValueError(f"{name} must be dense within a page")
+            raise ValueError("a cache must be dense within a page")
         n *= size
     return (t.stride(0) if t.shape[0] > 1 else n) * t.element_size()
 
@@ -152,21 +152,23 @@ def _cache_struct(name: str, c: Cache) -> CsaCache:
     if kind is None:
         raise ValueError(f"unknown cache type {c.dtype!r}")
     data, scale = c.data, c.scale
-    shape = data.shape
-    want = torch.bfloat16 if kind == CSA_CACHE_BF16 else torch.uint8
-    if len(shape) != 4 or (data.dtype != want and not (kind == CSA_CACHE_E4M3 and data.dtype == torch.float8_e4m3fn)):
-        raise TypeError(f"{name}.data must be a 4-dimensional {want} tensor")
-    D = shape[3] * 2 if kind == CSA_CACHE_E2M1 else shape[3]
+    dtype = data.dtype
+    if dtype != (torch.bfloat16 if kind == CSA_CACHE_BF16 else torch.uint8) and \
+            not (kind == CSA_CACHE_E4M3 and dtype == torch.float8_e4m3fn) or data.dim() != 4:
+        raise TypeError(f"{name}.data must be a 4-dimensional {'bfloat16' if kind == 0 else 'uint8'} tensor")
+    pages, H, page, D = data.shape
     if kind == CSA_CACHE_BF16:
-        return CsaCache(data.data_ptr(), None, kind, shape[1], D, shape[0], shape[2],
-                        _page_stride(name + ".data", data), 0, c.tensor_scale)
-    tail = shape[:3] if kind == CSA_CACHE_E4M3 else shape[:3] + (D // 16,)
-    want = torch.float32 if kind == CSA_CACHE_E4M3 else torch.uint8
-    if scale is None or scale.shape != tail or \
-            (scale.dtype != want and not (kind == CSA_CACHE_E2M1 and scale.dtype == torch.float8_e4m3fn)):
-        raise TypeError(f"{name}.scale must be {want} {tuple(tail)}")
-    return CsaCache(data.data_ptr(), scale.data_ptr(), kind, shape[1], D, shape[0], shape[2],
-                    _page_stride(name + ".data", data), _page_stride(name + ".scale", scale), c.tensor_scale)
+        return CsaCache(data.data_ptr(), None, kind, H, D, pages, page, _page_stride(data), 0, c.tensor_scale)
+    want = (pages, H, page)
+    if kind == CSA_CACHE_E2M1:
+        D *= 2
+        want = (pages, H, page, D // 16)
+    if scale is None or scale.shape != want or \
+            scale.dtype != (torch.float32 if kind == CSA_CACHE_E4M3 else torch.uint8) and \
+            not (kind == CSA_CACHE_E2M1 and scale.dtype == torch.float8_e4m3fn):
+        raise TypeError(f"{name}.scale must be {'float32' if kind == CSA_CACHE_E4M3 else 'uint8'} {want}")
+    return CsaCache(data.data_ptr(), scale.data_ptr(), kind, H, D, pages, page, _page_stride(data), _page_stride(scale),
+                    c.tensor_scale)
 
 
 def _on(dev, names, *tensors):
@@ -209,12 +211,17 @@ def _table(page_table, kv_len):
     """(kv_len, page_table, max_pages, table_stride) for the argument structs, after B."""
     import torch
 
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise TypeError("page_table must be int32 [B, max_pages] with dense rows")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise TypeError("page_table must be int32 [B, max_pages]")
     B, n = page_table.shape
-    lens = _int32("kv_len", kv_len, (B,))
-    return B, (lens, page_table.data_ptr(), n, page_table.stride(0) if B > 1 else n)
+    stride = n
+    if not page_table.is_contiguous():
+        if n > 1 and page_table.stride(1) != 1:
+            raise TypeError("page_table must have dense rows")
+        stride = page_table.stride(0) if B > 1 else n
+    if kv_len.dtype != torch.int32 or kv_len.shape != (B,) or not kv_len.is_contiguous():
+        raise TypeError(f"kv_len must be a contiguous int32 tensor of shape ({B},)")
+    return B, (kv_len.data_ptr(), page_table.data_ptr(), n, stride)
 
 
 @contextlib.contextmanager
@@ -355,7 +362,7 @@ def cache_append(k, cache_k: Cache, page_table, kv_len, *, v=None, cache_v: Opti
                       rope_scale)
     s, ctx = _launch(k, stream)
     with ctx:
-        st = csa_cache_append(a, s)
+        st = L.load_library().csa_cache_append(ctypes.byref(a), s)
     if st:
         raise L.CsaError(st, "csa_cache_append")
 
@@ -375,7 +382,7 @@ def cache_read(cache: Cache, page_table, kv_len, T: int, *, out=None, stream=Non
     with ctx:
         if out is None:
             out = cache.data.new_empty(shape, dtype=torch.bfloat16)
-        st = csa_cache_read(CsaCacheReadArgs(c, *pages, B, shape[1], out.data_ptr()), s)
+        st = L.load_library().csa_cache_read(ctypes.byref(CsaCacheReadArgs(c, *pages, B, shape[1], out.data_ptr())), s)
     if st:
         raise L.CsaError(st, "csa_cache_read")
     return out
@@ -412,12 +419,13 @@ def cache_attention(q, cache_k: Cache, cache_v: Cache, page_table, kv_len, *, sc
             lse = q.new_empty((B, S, HA), dtype=torch.float32)
         a = CsaCacheAttnArgs(q.data_ptr(), kc, vc, *pages, ip, topk, B, S, HA, bool(causal), scale, out.data_ptr(),
                              None if lse is None else lse.data_ptr())
+        lib, a = L.load_library(), ctypes.byref(a)
         if workspace is None:
-            size = csa_cache_attention_workspace_size(a)
+            size = lib.csa_cache_attention_workspace_size(a)
             ws = q.new_empty(size, dtype=torch.uint8) if size else None
         else:
             ws, size = workspace, workspace.numel() * workspace.element_size()
-        st = csa_cache_attention(a, None if ws is None else ws.data_ptr(), size, s)
+        st = lib.csa_cache_attention(a, None if ws is None else ws.data_ptr(), size, s)
     if st:
         raise L.CsaError(st, "csa_cache_attention")
     return (out, lse) if return_lse else out

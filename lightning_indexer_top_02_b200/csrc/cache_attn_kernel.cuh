@@ -83,7 +83,8 @@ struct AttnParams {
     float *lse;
     long long wait_limit;
     int splits;                             // wide kernel: shares of the keys
-    int ctas;                               // CTAs that share the chunks; 0: one a row tile (at most a chunk each)
+    int ctas;                               // CTAs that share the chunks; 0: one a row tile
+    int most;                               // chunks of a row tile, at most
     int works;                              // row tiles of a sequence
     int chunk;                              // keys that are shared out together
     int tiles;                              // row tiles of a group
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
     __syncthreads();
     next_kernel_may_begin();
     // the CTA's share: `left` chunks from chunk y of sequence `seq` on
-    long long left = 1, y = 0;
+    long long left = p.most, y = 0;
     int seq = 0;
     if (p.ctas) {
         const long long total = chunks_before(p, p.B, scratch);
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
     uint32_t phase = 0;                                  // of the staging barriers
     int at = 0;                                          // stage of the next block
     while (left > 0) {
-        int work = blockIdx.x, lo = 0, hi = 1, all = 1;      // the segment: chunks lo .. hi - 1 of `all`
+        int work = blockIdx.x, lo = 0, hi = p.most, all = p.most;   // the segment: chunks lo .. hi - 1 of `all`
         if (p.ctas) {
             all = chunks_of(p, seq);
             if (all <= 0)

@@ -23,6 +23,7 @@ struct CattnPlan {
     long long works, piece_rows;
     size_t workspace;
     int chunk;              // keys that are shared out together
+    int most;               // of the register kernel: chunks of a row tile, at most
     int ctas;               // of the register kernel: those that share the chunks, 0: one a row tile
     CattnFn fn;
     CattnWideFn wide_fn;

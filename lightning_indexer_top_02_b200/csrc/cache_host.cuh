@@ -501,10 +501,14 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
         }
     } else {
         // as many CTAs as the GPU holds share the chunks; where no tile has more
-        // than one chunk, a CTA each, and nothing to join
+        // than kAlone chunks, a CTA each, and no second kernel (one sequence of 777 keys, 8
+        // heads: 10.7 us on the device alone, 9.7 shared and joined, but 17 and 21 as issued;
+        // 16 such: 11.0 and 17.1)
+        constexpr long long kAlone = 4;
         const long long chunks = (most + pl->chunk - 1) / pl->chunk;
         const long long held = static_cast<long long>(sms) * pl->ctas;
-        pl->ctas = chunks <= 1 ? 0 : static_cast<int>(pl->works * chunks < held ? pl->works * chunks : held);
+        pl->most = static_cast<int>(chunks);
+        pl->ctas = chunks <= kAlone ? 0 : static_cast<int>(pl->works * chunks < held ? pl->works * chunks : held);
     }
     pl->splits = static_cast<int>(splits < 1 ? 1 : splits > 256 ? 256 : splits);
     if (pl->works * pl->splits >= kIntLimit)
@@ -641,6 +645,7 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     p.wait_limit = static_cast<long long>(g_wait_limit);
     p.splits = pl.splits;
     p.ctas = pl.ctas;
+    p.most = pl.most;
     p.chunk = pl.chunk;
     p.works = static_cast<int>(pl.works / a->B);
     p.tiles = pl.tiles;
