@@ -142,7 +142,11 @@ def _page_stride(t):
         if size != 1 and stride != n:
             raise ValueError("a cache must be dense within a page")
         n *= size
-    return (t.stride(0) if t.shape[0] > 1 else n) * t.element_size()
+    if t.shape[0] == 1:
+        return n * t.element_size()
+    if t.stride(0) < n:                     # (0 would be taken for dense)
+        raise ValueError("the pages of a cache must not overlap")
+    return t.stride(0) * t.element_size()
 
 
 def _cache_struct(name: str, c: Cache) -> CsaCache:

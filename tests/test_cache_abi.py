@@ -219,3 +219,18 @@ def test_binding_refuses():
         L.cache_append(q, c, table, lens, v=q)
     with pytest.raises(ValueError):
         L.cache_append(q[0], c, table, lens)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "e2m1"])
+def test_binding_refuses_overlapping_pages(dtype):
+    """Pages laid over one another (an expanded tensor's): neither dense nor strided."""
+    one, many = L.make_cache(dtype, 1, 16, 2, 64, device="cpu"), L.make_cache(dtype, 4, 16, 2, 64, device="cpu")
+    table, lens = torch.zeros((1, 4), dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    n = one.data[0].numel()
+    for data in (one.data.expand(4, -1, -1, -1), many.data.as_strided(many.data.shape, (n // 2,) + many.data.stride()[1:])):
+        with pytest.raises(ValueError, match="overlap"):
+            L.cache_read(L.Cache(dtype, data, many.scale), table, lens, 4)
+    if dtype != "bf16":
+        scale = one.scale.expand(4, *one.scale.shape[1:])
+        with pytest.raises(ValueError, match="overlap"):
+            L.cache_read(L.Cache(dtype, many.data, scale), table, lens, 4)
