@@ -397,7 +397,7 @@ def cache_attention(q, cache_k: Cache, cache_v: Cache, page_table, kv_len, *, sc
     """Attention of ``q`` bf16 [B,S,HA,Dk] over 4-bit caches: every visible
     position, or those of ``idx`` int32 [B,S,topk].  Returns ``out`` bf16
     [B,S,HA,Dv], with ``return_lse`` (out, lse fp32 [B,S,HA]).
-    ``workspace`` (uint8 CUDA tensor) is allocated if not given."""
+    ``workspace`` (dense uint8 CUDA tensor) is allocated if not given."""
     import torch
 
     dev = q.get_device()
@@ -413,6 +413,8 @@ def cache_attention(q, cache_k: Cache, cache_v: Cache, page_table, kv_len, *, sc
                                   ("lse", lse, torch.float32, (B, S, HA))):
         if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
             raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    if workspace is not None and not workspace.is_contiguous():
+        raise TypeError("workspace must be contiguous")
     _on(dev, "q cache_k.data cache_k.scale cache_v.data cache_v.scale page_table kv_len idx out lse workspace", q,
         cache_k.data, cache_k.scale, cache_v.data, cache_v.scale, page_table, kv_len, idx, out, lse, workspace)
     s, ctx = _launch(q, stream)

@@ -234,3 +234,13 @@ def test_binding_refuses_overlapping_pages(dtype):
         scale = one.scale.expand(4, *one.scale.shape[1:])
         with pytest.raises(ValueError, match="overlap"):
             L.cache_read(L.Cache(dtype, many.data, scale), table, lens, 4)
+
+
+def test_binding_refuses_spread_workspace():
+    """An expanded tensor counts more bytes than it has."""
+    c = L.make_cache("e2m1", 4, 16, 2, 128, device="cpu")
+    table, lens = torch.zeros((1, 4), dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    q = torch.zeros((1, 1, 4, 128), dtype=torch.bfloat16)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 20, dtype=torch.uint8)[::2]):
+        with pytest.raises(TypeError, match="workspace"):
+            L.cache_attention(q, c, c, table, lens, scale=1.0, workspace=ws)
