@@ -17,7 +17,7 @@
  * and holds the D elements x of one position:
  *   CSA_CACHE_BF16  D bf16 values; no scale
  *   CSA_CACHE_E4M3  D bytes and one fp32 scale: x ~ scale * E4M3, scale =
- *                   max|x| / 448 (1 for a row of zeros) -- the indexer's keys:
+ *                   max|x| / 448 (1 where that is 0 in fp32) -- the indexer's keys:
  *                   with H = 1 and one page of T rows a sequence, data is
  *                   csa_indexer's k [B,T,d] and scale its k_scale [B,T]
  *   CSA_CACHE_E2M1  D/2 bytes (the even element in a byte's low half) and

@@ -115,7 +115,8 @@ __device__ __forceinline__ void store16(const CacheView &c, uint8_t *data, uint8
             peak = 0.0f;
         for (int m = 1; m < lanes; m <<= 1)
             peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, m));
-        const float s = peak > 0.0f ? __fdiv_rn(peak, 448.0f) : 1.0f;
+        float s = __fdiv_rn(peak, 448.0f);
+        s = s > 0.0f ? s : 1.0f;                        // (0 for a peak below 2^-141, too: codes of zero)
         if (active) {
             uint4 w;
             uint32_t *u = reinterpret_cast<uint32_t *>(&w);

@@ -3,7 +3,7 @@
 //   (a, b) -> (a c - b s, b c + a s),  c + i s = scale * e^(i pos f_i).
 //
 // Bound by memory: 2 * sizeof(element) bytes an element against about three
-// flops.  One block takes kTokens tokens (and a share of their heads when there
+// flops.  One block takes a few tokens (and a share of their heads when there
 // are few tokens); its threads compute the tokens' cos and sin once, in
 // shared memory, and use them for every head, so the angles cost rot_dim / 2
 // sincospi a token and no table is read from memory.  What it took to reach memory's

@@ -229,6 +229,24 @@ def test_append_extremes(lib):
     no_device_error(L)
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "e2m1"])
+def test_append_vanishing_rows(lib, kind):
+    """Rows whose scale is too small for its type are rows of zeros, not of 0 / 0."""
+    L = lib
+    c = L.make_cache(kind, 2, 4, 1, 64, device="cuda")
+    table = torch.arange(2, dtype=torch.int32, device="cuda").view(2, 1)
+    k = torch.full((2, 4, 1, 64), 2.0 ** -100, dtype=torch.bfloat16, device="cuda")
+    k[:, :, :, 1::2] = 0
+    pos = torch.zeros((2, 4), dtype=torch.int32, device="cuda")
+    # rotated: 2^-145, and 2^-145 / 448 is 0 in fp32
+    L.cache_append(k, c, table, torch.full((2,), 4, dtype=torch.int32, device="cuda"), inv_freq=torch.ones(32, device="cuda"),
+                   positions=pos, rope_scale=2.0 ** -45)
+    no_device_error(L)
+    assert (R.held(kind, c.data, c.scale) == 0).all()
+    assert (c.scale == (1.0 if kind == "e4m3" else 0)).all()
+    assert (L.cache_read(c, table, torch.full((2,), 4, dtype=torch.int32, device="cuda"), 4) == 0).all()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "e2m1"])
 @pytest.mark.parametrize("B,T,H,D,page", [(1, 1, 1, 64, 1), (3, 100, 2, 128, 16), (4, 77, 3, 192, 24), (2, 50, 1, 512, 7), (3, 65, 8, 32, 64)])
 def test_read(lib, kind, B, T, H, D, page):
