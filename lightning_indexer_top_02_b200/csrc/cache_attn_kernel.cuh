@@ -514,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
                 qf[n][s][1] = f16x2_of(x[4 * s + 2] * down, x[4 * s + 3] * down);
             }
             // the scale's sign goes with the query, and the factor is not zero, so that a masked
-        // score times it is -inf
-        const float fr = fmaxf(up * fabsf(p.sl2), 1.17549435e-38f);
+            // score times it is -inf
+            const float fr = fmaxf(up * fabsf(p.sl2), 1.17549435e-38f);
             const int see = r < p.rows && len > 0 ? seen(p, len, i) : 0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
