@@ -27,8 +27,11 @@
 // significant bits and lies within 2^-10 .. 2688 or is zero.  A query row is scaled by a
 // power of two to a largest magnitude in [1, 2): what bf16 holds down to
 // 2^-14 of it stays exact, smaller elements are off by at most 2^-25 of the largest.
-// P is f16 (11 bits), at most 2^8 where the running maximum lags; sums,
-// maxima and O are fp32.
+// P is f16 (11 bits), relative to a reference 2^7 below the running maximum: the row's
+// largest is 2^7 at first and 2^13 at most where the maximum lags, so that half of f16's
+// smallest step is at most 2^-32 of the largest weight (relative to the maximum itself it would
+// be 2^-25, and what 2^17 keys that far below one leave would be lost).  Sums, maxima and O are
+// fp32.
 //
 // Tensor-core work here is mma.sync on purpose: tcgen05 reads operands from
 // shared memory, where writing the converted tile and reading it back would
@@ -65,7 +68,8 @@ using cache::PageMap;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kLag = 8.0f;                // the maximum is raised past 2^8 only
+constexpr float kHead = 7.0f;               // a row's reference: its maximum / 2^kHead when it was last raised
+constexpr float kLag = 13.0f;               // and it is raised when a weight would pass 2^kLag (f16: below 2^16)
 constexpr int kNoKey = 0x7FFFFFFF;          // a position no query sees
 
 struct AttnParams {
@@ -749,6 +753,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1)
                             best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
+                        best -= kHead;
                         if (best > m[n][c]) {
                             const float a = ex2_approx(m[n][c] - best);   // first keys: 2^-inf = 0
                             m[n][c] = best;

@@ -633,8 +633,8 @@ __device__ void wide_softmax(const WideParams &wp, uint8_t *smem, WideBarriers *
                 const float top = best == -INFINITY ? -INFINITY : best * f;
                 float alpha = 1.0f;
                 if (top > m + kLag) {                          // (first keys: m is -inf)
-                    alpha = ex2_approx(m - top);
-                    m = top;
+                    alpha = ex2_approx(m - (top - kHead));
+                    m = top - kHead;
                 }
                 // a raised maximum rescales O once the tile before is in it
                 if (t > cur.t0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
