@@ -25,8 +25,8 @@
 //     transposes the packed pairs into the B operand.
 // Values are exact in f16: an E2M1 code times an E4M3 scale has six
 // significant bits and lies within 2^-10 .. 2688 or is zero.  A query row is scaled by a
-// power of two to a largest magnitude in [1, 2): what bf16 holds down to
-// 2^-14 of it stays exact, smaller elements are off by at most 2^-25 of the largest.
+// power of two to a largest magnitude in [2^14, 2^15): what bf16 holds down to
+// 2^-28 of it stays exact, smaller elements are off by at most 2^-39 of the largest.
 // P is f16 (11 bits), relative to a reference 2^7 below the running maximum: the row's
 // largest is 2^7 at first and 2^13 at most where the maximum lags, so that half of f16's
 // smallest step is at most 2^-32 of the largest weight (relative to the maximum itself it would
@@ -275,6 +275,21 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The power of two over which a query row of largest magnitude `peak` is held in f16: its
+// largest is then in [2^14, 2^15), or smaller for a peak below 2^-112 (the unit and its inverse
+// are normal numbers).
+__device__ __forceinline__ float query_unit(float peak)
+{
+    const int e = min(max(static_cast<int>(__float_as_uint(peak) >> 23), 15), 254);
+    return __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+}
+
+// Its inverse, exactly.
+__device__ __forceinline__ float inverse_unit(float unit)
+{
+    return __uint_as_float((254u << 23) - __float_as_uint(unit));
+}
+
 // Byte j (constant after unrolling) of a packed word as an f16 pair.
 __device__ __forceinline__ uint32_t pair_of(uint32_t w, int j)
 {
@@ -508,10 +523,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
             }
             peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
             peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
-            // exponents of the scale and of its inverse, both normal powers of two
-            const int e = min(max(static_cast<int>(__float_as_uint(peak) >> 23), 1), 253);
-            const float down = __uint_as_float((static_cast<uint32_t>(254 - e) << 23) | (p.sl2 < 0.0f ? 0x80000000u : 0u));
-            const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+            const float up = query_unit(peak), down = p.sl2 < 0.0f ? -inverse_unit(up) : inverse_unit(up);
 #pragma unroll
             for (int s = 0; s < 4 * NG; ++s) {
                 qf[n][s][0] = f16x2_of(x[4 * s] * down, x[4 * s + 1] * down);

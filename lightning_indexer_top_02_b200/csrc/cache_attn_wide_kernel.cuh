@@ -471,11 +471,7 @@ __device__ __forceinline__ float wide_query(const AttnParams &p, const __nv_bflo
             }
         }
     }
-    const int e = min(max(static_cast<int>(__float_as_uint(peak) >> 23), 1), 253);
-    float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-    const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
-    if (p.sl2 < 0.0f)
-        down = -down;
+    const float up = query_unit(peak), down = p.sl2 < 0.0f ? -inverse_unit(up) : inverse_unit(up);
 #pragma unroll
     for (int c = 0; c < kDk; c += kPart) {
         if (!kKeep)

@@ -1,5 +1,5 @@
-"""How far the cache operators' arithmetic reaches: keys far below a row's largest
-(needs a B200).
+"""How far the cache operators' arithmetic reaches: keys far below a row's
+largest, query elements far below theirs (needs a B200).
 
 Bounds:
 * attention: P is f16 relative to 2^7 at least, so an absolute error of 2^-25 is 2^-32 of the
@@ -10,6 +10,8 @@ import math
 
 import pytest
 import torch
+
+import cache_ref as R
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +70,30 @@ def test_attention_weights_far_below_the_largest(lib, HA, D, log2):
     assert (out.double() - ref).abs().max() <= tol
     want = log2 * math.log(2.0) + math.log(mass)
     assert (lse.double() - want).abs().max() <= e + 2.0 ** -20 * (1 + want)
+
+
+@pytest.mark.parametrize("HA", [8, 16, 64, 128])
+@pytest.mark.parametrize("D", [64, 128, 192])
+@pytest.mark.parametrize("low", [2.0 ** -18, 2.0 ** -24])
+def test_attention_small_query_elements(lib, HA, D, low):
+    """One query element is far larger than the others and meets zeros only: the others
+    decide the softmax, and none of their bits is lost."""
+    L, n = lib, 700
+    g = torch.Generator(device="cuda").manual_seed(D + HA)
+    rows = lambda: R.stored(torch.randn((n, D), generator=g, device="cuda"), "e2m1")  # noqa: E731
+    kd, ks = rows()
+    kd[:, 0] &= 0xF0                                     # element 0 of every key: zero
+    vd, vs = rows()
+    q = torch.randn((1, 1, HA, D), generator=g, device="cuda")
+    q = (q.sign() * (0.5 + q.abs().clamp(max=3.0)) * low).to(torch.bfloat16)             # low / 2 .. 3.5 low
+    q[..., 0] = 1.0
+    scale = D ** -0.5 / low
+    table, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.tensor([n], dtype=torch.int32, device="cuda")
+    out, lse = L.cache_attention(q, dense(L, kd, ks), dense(L, vd, vs), table, lens, scale=scale, return_lse=True)
+    no_device_error(L)
+    k, v = R.held("e2m1", kd, ks)[:, None], R.held("e2m1", vd, vs)[:, None]
+    ref, rl, mean, size = R.attention(q[0, 0], k, v, torch.ones(n, dtype=torch.bool, device="cuda"), scale)
+    e = D * 2.0 ** -22 * size[:, None]
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2 * e) * mean * 1.01 + n * 2.0 ** -32 * v.abs().max()
+    assert ((out[0, 0].double() - ref).abs() <= tol).all()
+    assert ((lse[0, 0].double() - rl).abs() <= e[:, 0] + 2.0 ** -20 * (1 + rl.abs())).all()
