@@ -85,8 +85,8 @@ csa_status_t csa_rope_frequencies(int rot_dim, double base, int scaling, double 
  * a and b are elements rot_offset + i and rot_offset + i + rot_dim/2 of the
  * head, or rot_offset + 2i and + 2i + 1 (interleaved); the head's other
  * elements are copied.  The inverse applied to the gradient of the output is
- * the gradient of x.  Angles are reduced in double, so far positions lose
- * nothing; cos, sin and the products are fp32, rounded once to the element
+ * the gradient of x.  Angles are reduced in two doubles, so the farthest positions
+ * lose nothing; cos, sin and the products are fp32, rounded once to the element
  * type.  out == x (with equal strides) rotates in place; otherwise they must
  * not overlap.  rot_dim and rot_offset are even, rot_dim >= 2,
  * rot_offset + rot_dim <= D <= 1024; strides are in elements, heads and tokens must not

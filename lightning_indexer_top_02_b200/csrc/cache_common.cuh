@@ -171,13 +171,18 @@ __device__ __forceinline__ void load32(const void *src, uint4 &a, uint4 &b)
     }
 }
 
-// The angle pos * freq as a fraction of half turns in [-1, 1], reduced in
-// double: the product is exact (31 + 24 bits), 1 / 2 pi costs one rounding, so
-// the reduced angle is good to 2^-52 of the turns taken, at any position.
+// The angle pos * freq as a fraction of half turns, about [-1, 1].  The product has 31 + 24 bits,
+// two more than a double: it is kept as a rounded value and its exact remainder (fma), and the
+// quotient by 2 pi likewise, with 1 / 2 pi as two doubles.  What is left out is below 2^-104 of
+// the turns taken (2^-75 of a turn at the farthest position) beside the result's own rounding.
 __device__ __forceinline__ double half_turns(int pos, float freq)
 {
-    const double t = static_cast<double>(pos) * static_cast<double>(freq) * 0.15915494309189533577;
-    return 2.0 * (t - rint(t));
+    constexpr double kInv = 0.15915494309189535, kInvLow = -9.839338337591243e-18;   // 1 / 2 pi
+    const double p = pos, f = freq;
+    const double hi = p * f, lo = fma(p, f, -hi);
+    const double t = hi * kInv;
+    const double rest = fma(hi, kInv, -t) + fma(hi, kInvLow, lo * kInv);
+    return 2.0 * ((t - rint(t)) + rest);
 }
 
 } // namespace cache

@@ -1,12 +1,17 @@
 """How far the cache operators' arithmetic reaches: keys far below a row's
-largest, query elements far below theirs (needs a B200).
+largest, query elements far below theirs, angles of far positions (needs a B200).
 
 Bounds:
 * attention: P is f16 relative to 2^7 at least, so an absolute error of 2^-25 is 2^-32 of the
   largest weight; the rest as in test_gpu_cache.py (2^-11 of P, 2^-8 of out, a logit's
-  e = Dk * 2^-22 * scale * sum |q| |k|).
+  e = Dk * 2^-22 * scale * sum |q| |k|);
+* rotary: half turns are rounded to fp32 (at most 2^-25 of a half turn: 9.36e-8 rad) and
+  sincospi is good to one step of a value below one (5.97e-8); with pairs (1, 0) and a
+  factor of one nothing else rounds: 1.54e-7;
+* append: the stored value is the exactly rotated one, rounded to fp32 and to bf16.
 """
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -97,3 +102,77 @@ def test_attention_small_query_elements(lib, HA, D, low):
     tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2 * e) * mean * 1.01 + n * 2.0 ** -32 * v.abs().max()
     assert ((out[0, 0].double() - ref).abs() <= tol).all()
     assert ((lse[0, 0].double() - rl).abs() <= e[:, 0] + 2.0 ** -20 * (1 + rl.abs())).all()
+
+
+# ---------------------------------------------------------------- angles
+
+def pi_fraction(bits=256):
+    """pi from Machin's formula, in integers."""
+    one = 1 << (bits + 32)
+
+    def arctan_of_inverse(x):
+        term = total = one // x
+        n, sign = 3, -1
+        while term:
+            term //= x * x
+            total += sign * (term // n)
+            n, sign = n + 2, -sign
+        return total
+
+    return Fraction(4 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239)), one)
+
+
+def exact_cos_sin(pos, freq):
+    """cos and sin [N, half] of pos * freq, the angle reduced in rational arithmetic."""
+    inv = 1 / (2 * pi_fraction())
+    c, s = [], []
+    for f in [Fraction(x) * inv for x in freq.double().tolist()]:
+        col = []
+        for p in pos.tolist():
+            t = p * f
+            col.append(2 * math.pi * float(t - round(t)))
+        c.append([math.cos(a) for a in col])
+        s.append([math.sin(a) for a in col])
+    return torch.tensor(c, dtype=torch.float64).T.cuda(), torch.tensor(s, dtype=torch.float64).T.cuda()
+
+
+def far_positions(n, seed):
+    """Near both ends of int32, and between."""
+    g = torch.Generator().manual_seed(seed)
+    p = 2 ** 31 - 1 - torch.randint(0, 1 << 20, (n,), generator=g)
+    p[::4] = -p[::4]
+    p[1::8] = torch.randint(1 << 29, 1 << 31, (len(p[1::8]),), generator=g)
+    return p.to(torch.int32).cuda()
+
+
+def test_rotary_far_positions(lib):
+    L = lib
+    freq, _ = L.rope_frequencies(64, device="cuda")
+    pos = far_positions(256, 1)
+    x = torch.zeros((256, 1, 64), device="cuda")
+    x[..., :32] = 1.0
+    got = L.rotary(x, pos, freq)[:, 0].double()
+    c, s = exact_cos_sin(pos, freq.cpu())
+    no_device_error(L)
+    assert (got[:, :32] - c).abs().max() <= 1.54e-7
+    assert (got[:, 32:] - s).abs().max() <= 1.54e-7
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_far_positions(lib, inter):
+    """What a bf16 cache holds of keys rotated by far positions, bit by bit."""
+    L, N, H = lib, 512, 8
+    g = torch.Generator(device="cuda").manual_seed(2)
+    freq, _ = L.rope_frequencies(64, device="cuda")
+    pos = far_positions(N, 3)
+    k = torch.randn((1, N, H, 64), generator=g, device="cuda").to(torch.bfloat16)
+    cache = L.make_cache("bf16", 1, N, H, 64, device="cuda")
+    table, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.tensor([N], dtype=torch.int32, device="cuda")
+    L.cache_append(k, cache, table, lens, positions=pos.view(1, N), inv_freq=freq, interleaved=inter)
+    no_device_error(L)
+    c, s = (t[:, None] for t in exact_cos_sin(pos, freq.cpu()))
+    x = k[0].double()
+    a, b = (x[..., 0::2], x[..., 1::2]) if inter else (x[..., :32], x[..., 32:])
+    u, w = a * c - b * s, b * c + a * s
+    want = torch.stack((u, w), -1).flatten(-2) if inter else torch.cat((u, w), -1)
+    assert torch.equal(cache.data[0].transpose(0, 1), want.float().to(torch.bfloat16))
