@@ -111,7 +111,7 @@ csa_status_t csa_rotary(const csa_rotary_args_t *args, cudaStream_t stream);
  * Appends new keys (and values) to paged caches.  The tokens are [B, S]
  * (cu_tokens NULL; N = B * S), or packed: sequence b's are rows
  * cu_tokens[b] .. cu_tokens[b+1]-1 of N, ascending from cu_tokens[0] = 0, rows
- * from cu_tokens[B] on are not read.  A sequence's n new tokens go to
+ * (and positions) from cu_tokens[B] on are not read.  A sequence's n new tokens go to
  * positions kv_len[b] - n .. kv_len[b] - 1 (those below 0 are dropped).
  * With inv_freq, keys are rotated as csa_rotary says by positions[n], or
  * by the token's position in the cache when positions is NULL; values are

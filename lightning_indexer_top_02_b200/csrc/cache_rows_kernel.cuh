@@ -12,6 +12,7 @@
 // 128 from 4 bits to bf16 13.9 us (5.8 TB/s).
 #pragma once
 #include "cache_common.cuh"
+#include "ptx.cuh"
 
 namespace csa {
 namespace cache {
@@ -231,7 +232,7 @@ struct RowWalk {
         const int i = round * step + threadIdx.x / lanes;
         r.tok = static_cast<int>(p.div_H.div(i < rows ? i : 0));
         r.head = i < rows && 16 * lane < D ? i - r.tok * p.H : -1;
-        if (r.head >= 0) {
+        if (r.head >= 0 && CSA_CHECK_INDEX(kChkAppendRow, n0 + r.tok, p.cu ? __ldg(p.cu + p.B) : p.N)) {
             r.own.load(row(r) + 16 * lane);
             if (partnered)
                 r.other.load(row(r) + partner);
@@ -275,7 +276,10 @@ __global__ void __launch_bounds__(kRowThreads, 8) append_kernel(const AppendPara
     extern __shared__ Turn turns[];                     // [tokens][half]
     __shared__ int s_page[kMaxTile], s_off[kMaxTile], s_pos[kMaxTile];
     const int n0 = blockIdx.x * p.tokens;
-    const int nt = min(p.tokens, p.N - n0);
+    const int end = p.cu ? min(p.N, __ldg(p.cu + p.B)) : p.N;      // rows behind the last sequence's are not read
+    if (n0 >= end)
+        return;
+    const int nt = min(p.tokens, end - n0);
     const RowWalk<kHow> kw(p, p.k, p.kt, p.kh, p.Dk, p.lanes_k, n0, nt);
     const RowWalk<kStill> vw(p, p.v, p.vt, p.vh, p.Dv, p.lanes_v, n0, nt);
     RowPart cur, next;
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) append_kernel(const AppendPara
             b = n / p.S;
             const int len = __ldg(p.kv_len + b);
             pos = len > 0 ? len - p.S + (n - b * p.S) : -1;
-        } else if (n < __ldg(p.cu + p.B)) {
+        } else {
             // the last b with cu[b] <= n: the sequence that holds row n
             int lo = 0, hi = p.B;
             while (hi - lo > 1) {

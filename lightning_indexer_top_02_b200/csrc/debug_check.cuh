@@ -32,7 +32,8 @@ enum CheckSite : int {
     kChkScoreBuf = 5,    // epilogue: key slot in the CTA's score buffer
     kChkListPos = 6,     // selector: candidate list position
     kChkSelOut = 7,      // select kernel: staging slot in shared memory
-    kChkOutSlot = 8      // select kernel: output slot of a query row
+    kChkOutSlot = 8,     // select kernel: output slot of a query row
+    kChkAppendRow = 9    // append: token whose row is read
 };
 
 // Records a failed check (index not in [0, bound)) in `word` unless an

@@ -1,0 +1,56 @@
+"""What calls of the cache operators touch beside their outputs (needs a B200)."""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(HERE)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import lightning_indexer_top_02_b200 as L
+    from lightning_indexer_top_02_b200.build import build
+    build()
+    L.load_library()
+    return L
+
+
+def run_script(text, **env):
+    r = subprocess.run([sys.executable, "-c", text.format(root=ROOT, here=HERE)], capture_output=True, text=True,
+                       env=dict(os.environ, **env), timeout=600)
+    assert r.returncode == 0 and "script ok" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+_APPEND_SCRIPT = r"""
+import sys
+sys.path.insert(0, {root!r})
+import torch, lightning_indexer_top_02_b200 as L
+assert L.LIB_PATH.endswith("libcsa_indexer_debug.so"), L.LIB_PATH
+for kind in ("bf16", "e4m3", "e2m1"):
+    for N, ends in ((40, [0, 7, 7, 20]), (3000, [0, 1, 2, 900]), (64, [0, 0, 0, 0]), (50, [0, 10, 30, 50])):
+        for rot in (0, 64):
+            k = torch.randn((N, 2, 128), device="cuda").to(torch.bfloat16)
+            v = torch.randn((N, 2, 64), device="cuda").to(torch.bfloat16)
+            ck, cv = (L.make_cache(kind, 200, 16, 2, D, device="cuda") for D in (128, 64))
+            table = torch.arange(180, dtype=torch.int32, device="cuda").view(3, 60)
+            lens = torch.full((3,), 900, dtype=torch.int32, device="cuda")
+            freq = L.rope_frequencies(rot, device="cuda")[0] if rot else None
+            L.cache_append(k, ck, table, lens, v=v, cache_v=cv, cu_tokens=torch.tensor(ends, dtype=torch.int32, device="cuda"),
+                           inv_freq=freq, positions=torch.zeros(N, dtype=torch.int32, device="cuda"))
+            assert L.csa_last_device_error(None) == L.CSA_OK, (kind, N, ends, rot)
+print("script ok")
+"""
+
+
+def test_append_reads_no_row_past_the_last_sequence(lib):
+    """The debug build checks every row that a packed append reads against cu_tokens[B].  (The rows are all there.)"""
+    from lightning_indexer_top_02_b200.build import build
+    run_script(_APPEND_SCRIPT, CSA_INDEXER_LIB=build(debug=True))
