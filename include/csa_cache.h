@@ -117,8 +117,10 @@ csa_status_t csa_rotary(const csa_rotary_args_t *args, cudaStream_t stream);
  * by the token's position in the cache when positions is NULL; values are
  * not.  A rotated element is rounded once to fp32 (the products are carried
  * in more than 32 bits, so that a stored code does not depend on the order of
- * operations) and then to the cache's type.  The two caches are different memory
- * with the same num_pages, page_size, H and dtype.  Rows that no token goes to are left as they were.
+ * operations) and then to the cache's type.  The two caches have the same num_pages,
+ * page_size, H and dtype.  Their codes and scales are four different memories (pages may
+ * interleave in one allocation; a shared byte is refused), and no row that is
+ * written overlaps k or v.  Rows that no token goes to are left as they were.
  */
 typedef struct {
     const void *k;               /* bf16 [N, H, Dk] at the strides below, 16-byte aligned */

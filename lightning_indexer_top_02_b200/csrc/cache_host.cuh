@@ -97,6 +97,56 @@ bool same_pages(const csa_cache_t &a, const csa_cache_t &b)
     return a.dtype == b.dtype && a.H == b.H && a.num_pages == b.num_pages && a.page_size == b.page_size;
 }
 
+// Memory in pieces: `count` of them, `bytes` each, `stride` from one to the next.
+struct Pieces {
+    uintptr_t at;
+    long long stride, bytes;
+    int count;
+
+    uintptr_t end() const { return at + static_cast<uintptr_t>(count - 1) * stride + bytes; }
+};
+
+Pieces data_of(const csa_cache_t &c, const CacheView &v)
+{
+    return {reinterpret_cast<uintptr_t>(v.data), v.page_stride,
+            static_cast<long long>(c.H) * c.page_size * v.row_bytes, c.num_pages};
+}
+
+Pieces scale_of(const csa_cache_t &c, const CacheView &v)
+{
+    return {reinterpret_cast<uintptr_t>(v.scale), v.scale_stride,
+            static_cast<long long>(c.H) * c.page_size * v.scale_bytes, c.num_pages};
+}
+
+long long floor_div(long long a, long long b) { return a / b - (a % b < 0); }      // b > 0
+
+// Whether two memories share a byte.  Exact, so that caches whose pages interleave in one
+// allocation are told from caches that overlap: pages at one distance need one division, others
+// (in ranges that overlap) one for each page of the shorter list.
+bool share(const Pieces &a, const Pieces &b)
+{
+    if (a.bytes <= 0 || b.bytes <= 0 || a.end() <= b.at || b.end() <= a.at)
+        return false;
+    const long long d = static_cast<long long>(b.at - a.at);
+    if (a.stride == b.stride && a.count > 1 && b.count > 1) {
+        // pieces j of b and i of a meet where -b.bytes < d + (j - i) * stride < a.bytes
+        long long k = floor_div(-b.bytes - d, a.stride) + 1;
+        k = k > 1 - a.count ? k : 1 - a.count;
+        return k < b.count && d + k * a.stride < a.bytes;
+    }
+    if (a.count > b.count)
+        return share(b, a);
+    for (int i = 0; i < a.count; ++i) {
+        // the first piece of b that ends behind piece i of a begins
+        const long long from = i * a.stride - d;
+        long long j = b.count > 1 ? floor_div(from - b.bytes, b.stride) + 1 : 0;
+        j = j > 0 ? j : 0;
+        if (j < b.count && j * b.stride < from + a.bytes && j * b.stride + b.bytes > from)
+            return true;
+    }
+    return false;
+}
+
 // Launches a kernel that may begin while the one before it on the stream ends; it waits
 // for that one's results itself (after_kernel_before).
 template <typename... P>
@@ -304,7 +354,7 @@ extern "C" csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStre
         st = validate_cache(a->cache_v);
     if (st != CSA_OK)
         return st;
-    if (a->v && (!same_pages(a->cache_k, a->cache_v) || a->cache_k.data == a->cache_v.data))
+    if (a->v && !same_pages(a->cache_k, a->cache_v))
         return CSA_ERR_INVALID_ARG;
     if (a->inv_freq && (a->rot_dim < 2 || a->rot_dim % 2 != 0 || a->rot_offset < 0 || a->rot_offset % 2 != 0 ||
                         a->rot_offset > a->cache_k.D - a->rot_dim || !std::isfinite(a->rope_scale) ||
@@ -322,6 +372,15 @@ extern "C" csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStre
         (a->v && (a->v_token_stride < 0 || a->v_head_stride < 0 || a->v_token_stride % 8 != 0 ||
                   a->v_head_stride % 8 != 0)))
         return CSA_ERR_INVALID_ARG;
+    // what is written must be different memory: codes and scales, of keys and of values
+    const CacheView ck = cache_view(a->cache_k), cv = a->v ? cache_view(a->cache_v) : ck;
+    const csa_cache_t &cache_v = a->v ? a->cache_v : a->cache_k;
+    const Pieces written[4] = {data_of(a->cache_k, ck), scale_of(a->cache_k, ck), data_of(cache_v, cv),
+                               scale_of(cache_v, cv)};
+    for (int i = 0; i < (a->v ? 4 : 2); ++i)
+        for (int j = 0; j < i; ++j)
+            if (share(written[i], written[j]))
+                return CSA_ERR_INVALID_ARG;
     const int sms = device_sms();
     if (sms <= 0)
         return CSA_ERR_CUDA;
@@ -342,9 +401,9 @@ extern "C" csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStre
     p.cu = a->cu_tokens;
     p.kv_len = a->kv_len;
     p.pm = page_map(a->cache_k, a->page_table, a->max_pages, a->table_stride);
-    p.ck = cache_view(a->cache_k);
+    p.ck = ck;
     if (a->v)
-        p.cv = cache_view(a->cache_v);
+        p.cv = cv;
     p.inv_freq = a->inv_freq;
     p.positions = a->positions;
     p.half = a->inv_freq ? a->rot_dim / 2 : 0;
