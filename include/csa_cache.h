@@ -143,8 +143,8 @@ csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStream_t stream
 
 /*
  * Reads positions 0 .. T-1 of every sequence back as bf16: out [B, T, H, D]
- * (dense, 16-byte aligned; with H = 1 csa_sparse_attention's k or v), zeros at
- * positions from kv_len[b] on and where there is no row.
+ * (dense, 16-byte aligned, over no row that is read; with H = 1 csa_sparse_attention's
+ * k or v), zeros at positions from kv_len[b] on and where there is no row.
  */
 typedef struct {
     csa_cache_t cache;
@@ -171,7 +171,8 @@ csa_status_t csa_cache_read(const csa_cache_read_args_t *args, cudaStream_t stre
  * is fp32, the probabilities are rounded to 16 bits for P.V, out to bf16.
  * D of each cache is 64, 128, 192 or 256; HA a multiple of H, HA / H <= 128;
  * the caches have the same H, num_pages and page_size, and may be the same one
- * (values that are the keys).  out must not overlap q.
+ * (values that are the keys).  out, lse and the workspace overlap neither one another
+ * nor q, idx (refused) or a cache.
  * `workspace` is device memory of csa_cache_attention_workspace_size(args)
  * bytes (shapes and the device's SM count decide it, not the data; 0 for arguments
  * that the call rejects, or when it needs none), 256-byte

@@ -147,6 +147,11 @@ bool share(const Pieces &a, const Pieces &b)
     return false;
 }
 
+Pieces one_piece(const void *p, long long bytes)
+{
+    return {reinterpret_cast<uintptr_t>(p), 0, p ? bytes : 0, 1};
+}
+
 // Launches a kernel that may begin while the one before it on the stream ends; it waits
 // for that one's results itself (after_kernel_before).
 template <typename... P>
@@ -493,6 +498,21 @@ namespace {
 
 using csa::cattn::CattnPlan;
 
+// Whether anything that a call writes shares memory with the query, the selection or
+// something else that it writes.
+bool cattn_overlaps(const csa_cache_attn_args_t *a, const void *workspace, size_t workspace_bytes)
+{
+    const long long queries = static_cast<long long>(a->B) * a->S, rows = queries * a->HA;
+    const Pieces all[5] = {one_piece(a->q, 2 * rows * a->cache_k.D), one_piece(a->idx, 4 * queries * a->topk),
+                           one_piece(a->out, 2 * rows * a->cache_v.D), one_piece(a->lse, 4 * rows),
+                           one_piece(workspace, static_cast<long long>(workspace_bytes))};
+    for (int i = 2; i < 5; ++i)
+        for (int j = 0; j < i; ++j)
+            if (share(all[i], all[j]))
+                return true;
+    return false;
+}
+
 csa_status_t validate_cattn(const csa_cache_attn_args_t *a)
 {
     if (!a || a->B < 0 || a->S < 0 || a->HA <= 0 || !std::isfinite(a->scale) || (a->idx && a->topk <= 0))
@@ -513,13 +533,13 @@ csa_status_t validate_cattn(const csa_cache_attn_args_t *a)
     st = validate_pages(a->kv_len, a->page_table, a->max_pages, a->table_stride, a->cache_k.page_size);
     if (st != CSA_OK)
         return st;
-    if (!a->q || !a->out || a->q == a->out || !aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->idx, 4) ||
+    if (!a->q || !a->out || !aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->idx, 4) ||
         !aligned(a->lse, 4))
         return CSA_ERR_INVALID_ARG;
     if (static_cast<long long>(a->S) * a->HA >= kIntLimit || (a->idx && a->topk >= kIntLimit) ||
         static_cast<long long>(a->B) * a->S * a->HA >= kIntLimit)
         return CSA_ERR_UNSUPPORTED;
-    return CSA_OK;
+    return cattn_overlaps(a, nullptr, 0) ? CSA_ERR_INVALID_ARG : CSA_OK;
 }
 
 csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
@@ -677,7 +697,7 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     if (ws) {
         if (workspace_bytes < pl.workspace)
             return CSA_ERR_WORKSPACE;
-        if (!aligned(ws, 256))
+        if (!aligned(ws, 256) || cattn_overlaps(a, ws, pl.workspace))
             return CSA_ERR_INVALID_ARG;
     } else if (pl.workspace && cudaMallocAsync(&ws, pl.workspace, stream) != cudaSuccess) {
         return CSA_ERR_CUDA;

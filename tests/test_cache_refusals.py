@@ -103,3 +103,28 @@ def test_append_shared_memory_byte_by_byte():
         assert append(k, v) == want, [(c.data, c.scale, c.page_stride, c.scale_page_stride, c.D, pages, page) for c in (k, v)]
         seen[want] += 1
     assert min(seen.values()) > 200, seen
+
+
+def attention(workspace=None, **fields):
+    """B = 2, S = 3, 8 heads of 64: q and out of 6,144 bytes, lse of 192, idx of 6 * 40 entries."""
+    a = C.CsaCacheAttnArgs()
+    a.cache_k, a.cache_v = cache(2, 1 << 26), cache(2, 1 << 27)
+    a.kv_len = a.page_table = 1 << 28
+    a.max_pages = a.table_stride = 4
+    a.B, a.S, a.HA, a.topk, a.causal, a.scale = 2, 3, 8, 40, 1, 0.1
+    a.q, a.out, a.lse, a.idx = 1 << 20, 1 << 21, 1 << 22, 1 << 23
+    for f, v in fields.items():
+        setattr(a, f, v)
+    return L.csa_cache_attention(a, workspace, 1 << 20, None)
+
+
+@pytest.mark.parametrize("size,other,other_size,field", [(6144, "q", 6144, "out"), (6144, "idx", 960, "out"), (192, "q", 6144, "lse"),
+                                                         (192, "out", 6144, "lse"), (192, "idx", 960, "lse")])
+def test_attention_refuses_overlapping_outputs(size, other, other_size, field):
+    at = dict(q=1 << 20, out=1 << 21, lse=1 << 22, idx=1 << 23)[other]
+    assert attention() == L.CSA_ERR_CUDA
+    for d in (0, 16, other_size - 16, 16 - size):
+        assert attention(**{field: at + d}) == L.CSA_ERR_INVALID_ARG, d
+    for d in (other_size, -size):
+        assert attention(**{field: at + d}) == L.CSA_ERR_CUDA, d
+    assert attention(lse=None, idx=None) == L.CSA_ERR_CUDA

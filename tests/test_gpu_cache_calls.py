@@ -54,3 +54,20 @@ def test_append_reads_no_row_past_the_last_sequence(lib):
     """The debug build checks every row that a packed append reads against cu_tokens[B].  (The rows are all there.)"""
     from lightning_indexer_top_02_b200.build import build
     run_script(_APPEND_SCRIPT, CSA_INDEXER_LIB=build(debug=True))
+
+
+def test_workspace_over_outputs_is_refused(lib):
+    L = lib
+    c = L.make_cache("e2m1", 64, 64, 1, 128, device="cuda")
+    table = torch.arange(64, dtype=torch.int32, device="cuda").view(1, 64)
+    lens = torch.tensor([4000], dtype=torch.int32, device="cuda")
+    buf = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+    inside = lambda at: buf[at:at + 2048].view(torch.bfloat16).view(1, 1, 8, 128)  # noqa: E731
+    q = torch.zeros((1, 1, 8, 128), dtype=torch.bfloat16, device="cuda")
+    for query, out in ((q, inside(0)), (q, inside(4096)), (inside(512), None)):
+        with pytest.raises(L.CsaError) as e:
+            L.cache_attention(query, c, c, table, lens, scale=0.1, out=out, workspace=buf)
+        assert e.value.status == L.CSA_ERR_INVALID_ARG
+    L.cache_attention(inside(0), c, c, table, lens, scale=0.1, out=inside(2048), workspace=buf[4096:])
+    torch.cuda.synchronize()
+    assert L.csa_last_device_error(None) == L.CSA_OK
