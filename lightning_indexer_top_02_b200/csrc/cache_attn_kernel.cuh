@@ -81,7 +81,7 @@ struct AttnParams {
     int topk;
     int B, S, HA, H, G;                     // G = HA / H
     int causal;
-    float sl2;                              // scale * k tensor scale * log2(e)
+    float sl2;                              // scale * k tensor scale * log2(e) / 2^kQueryBits
     float v_scale;
     __nv_bfloat16 *out;
     float *lse;
@@ -275,19 +275,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The power of two over which a query row of largest magnitude `peak` is held in f16: its
-// largest is then in [2^14, 2^15), or smaller for a peak below 2^-112 (the unit and its inverse
-// are normal numbers).
-__device__ __forceinline__ float query_unit(float peak)
+// A query row of largest magnitude `peak` is held in f16 times `down`, a power of two: its largest
+// is then in [2^14, 2^15), or smaller for a peak below 2^-112.  2^14 / down is `up`, both are normal
+// numbers, and 2^-14 is part of AttnParams::sl2 (as a step of its own here it cost the wide kernel
+// 1.1 us of 27 at 32 sequences x 128 heads x 2,048 keys).
+constexpr int kQueryBits = 14;
+__device__ __forceinline__ void query_scale(float peak, float &down, float &up)
 {
-    const int e = min(max(static_cast<int>(__float_as_uint(peak) >> 23), 15), 254);
-    return __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-}
-
-// Its inverse, exactly.
-__device__ __forceinline__ float inverse_unit(float unit)
-{
-    return __uint_as_float((254u << 23) - __float_as_uint(unit));
+    const int e = min(max(static_cast<int>(__float_as_uint(peak) >> 23), kQueryBits), 254);
+    down = __uint_as_float(static_cast<uint32_t>(254 + kQueryBits - e) << 23);
+    up = __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
 
 // Byte j (constant after unrolling) of a packed word as an f16 pair.
@@ -523,7 +520,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
             }
             peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
             peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
-            const float up = query_unit(peak), down = p.sl2 < 0.0f ? -inverse_unit(up) : inverse_unit(up);
+            float down, up;
+            query_scale(peak, down, up);
+            if (p.sl2 < 0.0f)
+                down = -down;
 #pragma unroll
             for (int s = 0; s < 4 * NG; ++s) {
                 qf[n][s][0] = f16x2_of(x[4 * s] * down, x[4 * s + 1] * down);

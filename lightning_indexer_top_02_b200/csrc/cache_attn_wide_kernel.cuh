@@ -471,7 +471,10 @@ __device__ __forceinline__ float wide_query(const AttnParams &p, const __nv_bflo
             }
         }
     }
-    const float up = query_unit(peak), down = p.sl2 < 0.0f ? -inverse_unit(up) : inverse_unit(up);
+    float down, up;
+    query_scale(peak, down, up);
+    if (p.sl2 < 0.0f)
+        down = -down;
 #pragma unroll
     for (int c = 0; c < kDk; c += kPart) {
         if (!kKeep)

@@ -717,7 +717,7 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     p.H = a->cache_k.H;
     p.G = p.HA / p.H;
     p.causal = a->causal != 0;
-    p.sl2 = a->scale * a->cache_k.tensor_scale * 1.4426950408889634f;
+    p.sl2 = a->scale * a->cache_k.tensor_scale * (1.4426950408889634f / (1 << csa::cattn::kQueryBits));
     p.v_scale = a->cache_v.tensor_scale;
     p.out = static_cast<__nv_bfloat16 *>(a->out);
     p.lse = a->lse;
