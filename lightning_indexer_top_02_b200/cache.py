@@ -4,8 +4,8 @@ cache, reading it back as bf16 rows, and attention over a cache held in 4 bits.
 The same calls as ``include/csa_cache.h`` (operation, layouts and limits are
 stated there), marshalled with ctypes; outputs and workspaces are allocated on
 the tensors' device if not given.  Nothing here records a gradient: a tensor
-that would need one is refused (``rotary(..., inverse=True)`` is the gradient
-of ``rotary``).
+that would need one, or that carries a forward-mode tangent, is refused
+(``rotary(..., inverse=True)`` is the gradient of ``rotary``).
 """
 from __future__ import annotations
 
@@ -176,16 +176,18 @@ def _cache_struct(name: str, c: Cache) -> CsaCache:
 
 
 def _on(dev, names, *tensors):
-    """Every tensor on one CUDA device, and none that would need a gradient.  (Checked
-    in one go, names looked up only for an error: this is on every call's path.)"""
+    """Every tensor on one CUDA device, and none that would need a gradient or carries a
+    tangent.  (Checked in one go, names looked up only for an error: this is on every
+    call's path.)"""
+    import torch
+
+    forward_ad = torch.autograd.forward_ad
     for t in tensors:
         if t is not None and (t.get_device() != dev or t.requires_grad):
             break
     else:
-        if dev >= 0:
+        if dev >= 0 and forward_ad._current_level < 0:
             return
-    import torch
-
     for name, t in zip(names.split(), tensors):
         if t is None:
             continue
@@ -193,6 +195,8 @@ def _on(dev, names, *tensors):
             raise ValueError(f"{name} must be on " + (f"CUDA device {dev}" if dev >= 0 else "a CUDA device"))
         if t.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"{name} needs a gradient, which this call does not record")
+        if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{name} carries a tangent, which this call does not pass on")
 
 
 def _int32(name, t, shape):

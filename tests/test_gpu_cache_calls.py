@@ -71,3 +71,33 @@ def test_workspace_over_outputs_is_refused(lib):
     L.cache_attention(inside(0), c, c, table, lens, scale=0.1, out=inside(2048), workspace=buf[4096:])
     torch.cuda.synchronize()
     assert L.csa_last_device_error(None) == L.CSA_OK
+
+
+# ---------------------------------------------------------------- autograd
+
+def step(L):
+    c = L.make_cache("e4m3", 2, 16, 1, 64, device="cuda")
+    x = torch.randn((1, 3, 1, 64), device="cuda").to(torch.bfloat16)
+    table = torch.arange(2, dtype=torch.int32, device="cuda").view(1, 2)
+    return c, x, table, torch.full((1,), 3, dtype=torch.int32, device="cuda"), torch.zeros((1, 3), dtype=torch.int32, device="cuda")
+
+
+def test_tangents_are_refused(lib):
+    """A tensor that carries a forward-mode tangent, which no call here would pass on."""
+    import torch.autograd.forward_ad as fw
+    L = lib
+    c, x, table, lens, pos = step(L)
+    freq = torch.ones(8, device="cuda")
+    with fw.dual_level():
+        d = fw.make_dual(x, torch.ones_like(x))
+        with pytest.raises(ValueError, match="tangent"):
+            L.rotary(d, pos, freq)
+        with pytest.raises(ValueError, match="tangent"):
+            L.cache_append(d, c, table, lens)
+        with pytest.raises(ValueError, match="tangent"):
+            L.cache_read(L.Cache("bf16", fw.make_dual(x, x)), table, lens, 1)
+        e = L.make_cache("e2m1", 2, 16, 1, 64, device="cuda")
+        with pytest.raises(ValueError, match="tangent"):
+            L.cache_attention(d, e, e, table, lens, scale=0.1)
+        assert torch.equal(L.rotary(x, pos, freq), x)    # (others pass; position 0)
+    assert torch.equal(L.rotary(d, pos, freq), x)        # the level has ended: an ordinary tensor
