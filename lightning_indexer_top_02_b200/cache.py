@@ -199,6 +199,14 @@ def _on(dev, names, *tensors):
             raise ValueError(f"{name} carries a tangent, which this call does not pass on")
 
 
+def _wrote(*tensors):
+    """Counts a change of the caller's tensors that a call writes through their
+    addresses, so that autograd refuses to use a value it had kept of them."""
+    import torch
+
+    torch.autograd.graph.increment_version(tensors)
+
+
 def _int32(name, t, shape):
     import torch
 
@@ -301,6 +309,8 @@ def rotary(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = F
     with ctx:
         if out is None:
             out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
+        else:
+            _wrote(out)
         if x.numel():
             os = xs if out is x else _token_strides("out", out)
             st = L.load_library().csa_rotary(
@@ -373,6 +383,8 @@ def cache_append(k, cache_k: Cache, page_table, kv_len, *, v=None, cache_v: Opti
         st = L.load_library().csa_cache_append(ctypes.byref(a), s)
     if st:
         raise L.CsaError(st, "csa_cache_append")
+    for c in (cache_k, cache_v) if cache_v is not None else (cache_k,):
+        _wrote(c.data) if c.scale is None else _wrote(c.data, c.scale)
 
 
 def cache_read(cache: Cache, page_table, kv_len, T: int, *, out=None, stream=None):
@@ -390,6 +402,8 @@ def cache_read(cache: Cache, page_table, kv_len, T: int, *, out=None, stream=Non
     with ctx:
         if out is None:
             out = cache.data.new_empty(shape, dtype=torch.bfloat16)
+        else:
+            _wrote(out)
         st = L.load_library().csa_cache_read(ctypes.byref(CsaCacheReadArgs(c, *pages, B, shape[1], out.data_ptr())), s)
     if st:
         raise L.CsaError(st, "csa_cache_read")
@@ -425,7 +439,11 @@ def cache_attention(q, cache_k: Cache, cache_v: Cache, page_table, kv_len, *, sc
     with ctx:
         if out is None:
             out = torch.empty_like(q) if vc.D == kc.D else q.new_empty((B, S, HA, vc.D))
-        if lse is None and return_lse:
+        else:
+            _wrote(out)
+        if lse is not None:
+            _wrote(lse)
+        elif return_lse:
             lse = q.new_empty((B, S, HA), dtype=torch.float32)
         a = CsaCacheAttnArgs(q.data_ptr(), kc, vc, *pages, ip, topk, B, S, HA, bool(causal), scale, out.data_ptr(),
                              None if lse is None else lse.data_ptr())

@@ -101,3 +101,37 @@ def test_tangents_are_refused(lib):
             L.cache_attention(d, e, e, table, lens, scale=0.1)
         assert torch.equal(L.rotary(x, pos, freq), x)    # (others pass; position 0)
     assert torch.equal(L.rotary(d, pos, freq), x)        # the level has ended: an ordinary tensor
+
+
+def test_writes_are_seen_by_autograd(lib):
+    """What a call writes counts as changed, so that a product's gradient is not computed from it."""
+    L = lib
+    c, x, table, lens, pos = step(L)
+    freq = torch.ones(8, device="cuda")
+    y = torch.randn_like(x).requires_grad_()
+    z = (x * y).sum()                                    # keeps x for y's gradient
+    L.rotary(x, pos + 1, freq, out=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward()
+
+    def changes(call, *tensors):
+        was = [t._version for t in tensors]
+        call()
+        return [t._version > w for t, w in zip(tensors, was)]
+
+    out = torch.empty_like(x)
+    assert changes(lambda: L.rotary(x, pos, freq, out=out), out, x) == [True, False]
+    assert changes(lambda: L.cache_append(x, c, table, lens), c.data, c.scale, x) == [True, True, False]
+    b = L.make_cache("bf16", 2, 16, 1, 64, device="cuda")
+    assert changes(lambda: L.cache_append(x, c, table, lens, v=x, cache_v=L.make_cache("e4m3", 2, 16, 1, 64, device="cuda")),
+                   c.data, c.scale) == [True, True]
+    assert changes(lambda: L.cache_append(x, b, table, lens), b.data) == [True]
+    out = torch.empty((1, 4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    assert changes(lambda: L.cache_read(c, table, lens, 4, out=out), out, c.data) == [True, False]
+    e = L.make_cache("e2m1", 2, 16, 1, 64, device="cuda")
+    out, lse = torch.empty_like(x), torch.empty((1, 3, 1), device="cuda")
+    assert changes(lambda: L.cache_attention(x, e, e, table, lens, scale=0.1, out=out, lse=lse), out, lse, x, e.data) == \
+        [True, True, False, False]
+    with torch.inference_mode():
+        t = torch.zeros((1, 3, 1, 64), dtype=torch.bfloat16, device="cuda")
+        L.rotary(t, pos, freq, out=t)                    # (no version to count)
