@@ -161,6 +161,8 @@ def _cache_struct(name: str, c: Cache) -> CsaCache:
             not (kind == CSA_CACHE_E4M3 and dtype == torch.float8_e4m3fn) or data.dim() != 4:
         raise TypeError(f"{name}.data must be a 4-dimensional {'bfloat16' if kind == 0 else 'uint8'} tensor")
     pages, H, page, D = data.shape
+    if data.numel() > _INT_MAX // 2:
+        _ints(**{f"{name}'s pages": pages, "H": H, "page_size": page, "D": 2 * D})
     if kind == CSA_CACHE_BF16:
         return CsaCache(data.data_ptr(), None, kind, H, D, pages, page, _page_stride(data), 0, c.tensor_scale)
     want = (pages, H, page)
@@ -199,6 +201,16 @@ def _on(dev, names, *tensors):
             raise ValueError(f"{name} carries a tangent, which this call does not pass on")
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _ints(**sizes):
+    """An argument struct's 32-bit fields would take larger numbers modulo 2^32."""
+    for name, n in sizes.items():
+        if not -_INT_MAX <= n <= _INT_MAX:
+            raise ValueError(f"{name} = {n} does not fit in 32 bits")
+
+
 def _wrote(*tensors):
     """Counts a change of the caller's tensors that a call writes through their
     addresses, so that autograd refuses to use a value it had kept of them."""
@@ -230,6 +242,8 @@ def _table(page_table, kv_len):
     if page_table.dtype != torch.int32 or page_table.dim() != 2:
         raise TypeError("page_table must be int32 [B, max_pages]")
     B, n = page_table.shape
+    if page_table.numel() > _INT_MAX:
+        _ints(B=B, max_pages=n)
     stride = n
     if not page_table.is_contiguous():
         if n > 1 and page_table.stride(1) != 1:
@@ -279,6 +293,7 @@ def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: str = "pla
 
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"unknown scaling {scaling!r}")
+    _ints(rot_dim=rot_dim, original_len=original_len)
     f = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float32)
     m = ctypes.c_float()
     _check(csa_rope_frequencies(rot_dim, base, ROPE_SCALINGS[scaling], factor, original_len, beta_fast,
@@ -301,6 +316,9 @@ def rotary(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = F
     dev = x.get_device()
     pos = _int32("positions", positions, shape[:-2])
     freq = _freq(inv_freq)
+    N, rot = positions.numel(), 2 * inv_freq.numel()
+    if x.numel() > _INT_MAX or rot > _INT_MAX or not -_INT_MAX < rot_offset < _INT_MAX:
+        _ints(tokens=N, H=shape[-2], D=shape[-1], rot_dim=rot, rot_offset=rot_offset)
     xs = _token_strides("x", x)
     if out is not None and (out.shape != shape or out.dtype != x.dtype):
         raise TypeError("out must have the shape and type of x")
@@ -314,8 +332,8 @@ def rotary(x, positions, inv_freq, *, rot_offset: int = 0, interleaved: bool = F
         if x.numel():
             os = xs if out is x else _token_strides("out", out)
             st = L.load_library().csa_rotary(
-                ctypes.byref(CsaRotaryArgs(x.data_ptr(), out.data_ptr(), kind, positions.numel(), shape[-2], shape[-1],
-                                           *xs, *os, pos, freq, 2 * inv_freq.numel(), rot_offset, bool(interleaved),
+                ctypes.byref(CsaRotaryArgs(x.data_ptr(), out.data_ptr(), kind, N, shape[-2], shape[-1],
+                                           *xs, *os, pos, freq, rot, rot_offset, bool(interleaved),
                                            bool(inverse), scale)), s)
             if st:
                 raise L.CsaError(st, "csa_rotary")
@@ -373,6 +391,8 @@ def cache_append(k, cache_k: Cache, page_table, kv_len, *, v=None, cache_v: Opti
     cu = _int32("cu_tokens", cu_tokens, (B + 1,)) if cu_tokens is not None else None
     pos = _int32("positions", positions, lead) if positions is not None else None
     freq, rot = (_freq(inv_freq), 2 * inv_freq.numel()) if inv_freq is not None else (None, 0)
+    if N > _INT_MAX or rot > _INT_MAX or not -_INT_MAX < rot_offset < _INT_MAX:
+        _ints(tokens=N, rot_dim=rot, rot_offset=rot_offset)
     _on(dev, "k cache_k.data cache_k.scale v cache_v.data cache_v.scale page_table kv_len cu_tokens positions inv_freq",
         k, cache_k.data, cache_k.scale, v, cache_v and cache_v.data, cache_v and cache_v.scale, page_table, kv_len,
         cu_tokens, positions, inv_freq)
@@ -394,7 +414,9 @@ def cache_read(cache: Cache, page_table, kv_len, T: int, *, out=None, stream=Non
     dev = cache.data.get_device()
     B, pages = _table(page_table, kv_len)
     c = _cache_struct("cache", cache)
-    shape = (B, int(T), c.H, c.D)
+    T = int(T)
+    _ints(T=T)
+    shape = (B, T, c.H, c.D)
     if out is not None and (out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous()):
         raise TypeError(f"out must be a contiguous bfloat16 tensor of shape {shape}")
     _on(dev, "cache.data cache.scale page_table kv_len out", cache.data, cache.scale, page_table, kv_len, out)
@@ -404,7 +426,7 @@ def cache_read(cache: Cache, page_table, kv_len, T: int, *, out=None, stream=Non
             out = cache.data.new_empty(shape, dtype=torch.bfloat16)
         else:
             _wrote(out)
-        st = L.load_library().csa_cache_read(ctypes.byref(CsaCacheReadArgs(c, *pages, B, shape[1], out.data_ptr())), s)
+        st = L.load_library().csa_cache_read(ctypes.byref(CsaCacheReadArgs(c, *pages, B, T, out.data_ptr())), s)
     if st:
         raise L.CsaError(st, "csa_cache_read")
     return out
@@ -424,6 +446,8 @@ def cache_attention(q, cache_k: Cache, cache_v: Cache, page_table, kv_len, *, sc
     if q.dtype != torch.bfloat16 or q.dim() != 4 or q.shape[0] != B or not q.is_contiguous() or q.shape[-1] != kc.D:
         raise TypeError("q must be a contiguous bfloat16 tensor [B, S, HA, Dk]")
     _, S, HA, _ = q.shape
+    if q.numel() > _INT_MAX or idx is not None and idx.numel() > _INT_MAX:
+        _ints(S=S, HA=HA, topk=0 if idx is None else idx.shape[-1])
     if idx is not None and idx.numel() == 0 and B * S:
         raise ValueError("idx has no entries (leave it out for every visible position)")
     ip, topk = (None, 0) if idx is None else (_int32("idx", idx, (B, S, idx.shape[-1])), idx.shape[-1])

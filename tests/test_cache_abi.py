@@ -244,3 +244,19 @@ def test_binding_refuses_spread_workspace():
     for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 20, dtype=torch.uint8)[::2]):
         with pytest.raises(TypeError, match="workspace"):
             L.cache_attention(q, c, c, table, lens, scale=1.0, workspace=ws)
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    """The argument structs' fields are 32 bits wide: larger numbers would arrive modulo 2^32."""
+    x, pos, f = torch.zeros(2, 4, 128), torch.zeros(2, dtype=torch.int32), torch.ones(32)
+    c = L.make_cache("e2m1", 4, 16, 2, 128, device="cpu")
+    table, lens = torch.zeros((1, 4), dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    k = torch.zeros((1, 1, 2, 128), dtype=torch.bfloat16)
+    cu = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: L.rotary(x, pos, f, rot_offset=2 ** 32), lambda: L.rotary(x, pos, f, rot_offset=-2 ** 32),
+                 lambda: L.cache_append(k, c, table, lens, inv_freq=f, rot_offset=2 ** 32),
+                 lambda: L.cache_append(k[0, 0].expand(2 ** 32 + 1, 2, 128), c, table, lens, cu_tokens=cu),
+                 lambda: L.cache_read(c, table, lens, 2 ** 32 + 4), lambda: L.rope_frequencies(2 ** 32 + 64),
+                 lambda: L.rope_frequencies(64, scaling="yarn", factor=2.0, original_len=2 ** 32 + 4096)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
