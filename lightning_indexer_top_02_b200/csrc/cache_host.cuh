@@ -361,6 +361,10 @@ extern "C" csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStre
         return st;
     if (a->v && !same_pages(a->cache_k, a->cache_v))
         return CSA_ERR_INVALID_ARG;
+    // the lanes that a token's rows take are counted in an int
+    if (static_cast<long long>(a->cache_k.H) * row_lanes(a->cache_k.D) >= kIntLimit ||
+        (a->v && static_cast<long long>(a->cache_v.H) * row_lanes(a->cache_v.D) >= kIntLimit))
+        return CSA_ERR_UNSUPPORTED;
     if (a->inv_freq && (a->rot_dim < 2 || a->rot_dim % 2 != 0 || a->rot_offset < 0 || a->rot_offset % 2 != 0 ||
                         a->rot_offset > a->cache_k.D - a->rot_dim || !std::isfinite(a->rope_scale) ||
                         !aligned(a->inv_freq, 4)))
@@ -419,7 +423,7 @@ extern "C" csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStre
     // tokens a block takes: about four rounds of rows, fewer while blocks are few
     int tokens = 4 * csa::cache::kRowThreads / (p.lanes_k * p.H);
     tokens = tokens < 1 ? 1 : tokens > csa::cache::kMaxTile ? csa::cache::kMaxTile : tokens;
-    while (tokens > 1 && (a->N + tokens - 1) / tokens < 4 * sms)
+    while (tokens > 1 && (static_cast<long long>(a->N) + tokens - 1) / tokens < 4ll * sms)
         tokens = (tokens + 1) / 2;
     const int turns = p.half + (p.half >> 3);            // places of a token's cos and sin (turn_at)
     if (p.half && tokens > 2048 / turns)                 // in 32 KB

@@ -128,3 +128,13 @@ def test_attention_refuses_overlapping_outputs(size, other, other_size, field):
     for d in (other_size, -size):
         assert attention(**{field: at + d}) == L.CSA_ERR_CUDA, d
     assert attention(lse=None, idx=None) == L.CSA_ERR_CUDA
+
+
+@pytest.mark.parametrize("dtype", [C.CSA_CACHE_BF16, C.CSA_CACHE_E4M3, C.CSA_CACHE_E2M1])
+def test_append_refuses_heads_past_an_int(dtype):
+    """2^30 heads of 4 lanes each: their product is 0 in 32 bits, which the host divided by."""
+    far = (1 << 40, 1 << 50)
+    assert append(cache(dtype, far, H=1 << 30, pages=1, page=1)) == L.CSA_ERR_UNSUPPORTED
+    k, v = (cache(dtype, at, H=1 << 28, D=D, pages=1, page=1) for at, D in ((far, 32), ((1 << 41, 1 << 51), 128)))
+    assert append(k, v) == L.CSA_ERR_UNSUPPORTED
+    assert append(k) == L.CSA_ERR_CUDA
