@@ -62,7 +62,8 @@ typedef struct {
     int num_pages, page_size;
     long long page_stride;       /* bytes from page to page, a multiple of 16; 0: dense  */
     long long scale_page_stride; /* bytes, a multiple of a row's scale bytes; 0: dense   */
-    float tensor_scale;          /* CSA_CACHE_E2M1: finite, > 0; others ignore it        */
+    float tensor_scale;          /* CSA_CACHE_E2M1: > 0 and finite (an append: 6 times   */
+                                 /* it, too); others ignore it                           */
 } csa_cache_t;
 
 /*
@@ -169,6 +170,7 @@ csa_status_t csa_cache_read(const csa_cache_read_args_t *args, cudaStream_t stre
  * (zeros and -inf where a row sees no key).  Arithmetic: the stored values
  * are exact in the tensor cores' 16-bit types; q.k and P.V accumulate in fp32, softmax
  * is fp32, the probabilities are rounded to 16 bits for P.V, out to bf16.
+ * scale times the keys' tensor_scale is finite in fp32.
  * D of each cache is 64, 128, 192 or 256; HA a multiple of H, HA / H <= 128;
  * the caches have the same H, num_pages and page_size, and may be the same one
  * (values that are the keys).  out, lse and the workspace overlap neither one another

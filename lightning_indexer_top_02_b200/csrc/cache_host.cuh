@@ -361,6 +361,10 @@ extern "C" csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStre
         return st;
     if (a->v && !same_pages(a->cache_k, a->cache_v))
         return CSA_ERR_INVALID_ARG;
+    // six tensor scales are what a code of the largest magnitude and a scale of one stand for
+    if (a->cache_k.dtype == CSA_CACHE_E2M1 && (!std::isfinite(6.0f * a->cache_k.tensor_scale) ||
+                                               (a->v && !std::isfinite(6.0f * a->cache_v.tensor_scale))))
+        return CSA_ERR_INVALID_ARG;
     // the lanes that a token's rows take are counted in an int
     if (static_cast<long long>(a->cache_k.H) * row_lanes(a->cache_k.D) >= kIntLimit ||
         (a->v && static_cast<long long>(a->cache_v.H) * row_lanes(a->cache_v.D) >= kIntLimit))
@@ -502,6 +506,12 @@ namespace {
 
 using csa::cattn::CattnPlan;
 
+// What turns a product of stored keys and a query (times 2^kQueryBits) into a log2 score.
+float log2_scale(const csa_cache_attn_args_t *a)
+{
+    return a->scale * a->cache_k.tensor_scale * (1.4426950408889634f / (1 << csa::cattn::kQueryBits));
+}
+
 // Whether anything that a call writes shares memory with the query, the selection or
 // something else that it writes.
 bool cattn_overlaps(const csa_cache_attn_args_t *a, const void *workspace, size_t workspace_bytes)
@@ -527,6 +537,8 @@ csa_status_t validate_cattn(const csa_cache_attn_args_t *a)
     if (st != CSA_OK)
         return st;
     if (!same_pages(a->cache_k, a->cache_v) || a->HA % a->cache_k.H != 0)
+        return CSA_ERR_INVALID_ARG;
+    if (a->cache_k.dtype == CSA_CACHE_E2M1 && !std::isfinite(log2_scale(a)))
         return CSA_ERR_INVALID_ARG;
     const int dk = a->cache_k.D, dv = a->cache_v.D;
     if (a->cache_k.dtype != CSA_CACHE_E2M1 || dk % 64 != 0 || dk > 256 || dv % 64 != 0 || dv > 256 ||
@@ -721,7 +733,7 @@ extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, v
     p.H = a->cache_k.H;
     p.G = p.HA / p.H;
     p.causal = a->causal != 0;
-    p.sl2 = a->scale * a->cache_k.tensor_scale * (1.4426950408889634f / (1 << csa::cattn::kQueryBits));
+    p.sl2 = log2_scale(a);
     p.v_scale = a->cache_v.tensor_scale;
     p.out = static_cast<__nv_bfloat16 *>(a->out);
     p.lse = a->lse;

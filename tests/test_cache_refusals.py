@@ -138,3 +138,16 @@ def test_append_refuses_heads_past_an_int(dtype):
     k, v = (cache(dtype, at, H=1 << 28, D=D, pages=1, page=1) for at, D in ((far, 32), ((1 << 41, 1 << 51), 128)))
     assert append(k, v) == L.CSA_ERR_UNSUPPORTED
     assert append(k) == L.CSA_ERR_CUDA
+
+
+def test_scales_whose_product_is_not_finite():
+    """Each is finite; their products, which the kernels compute with, are not."""
+    k = cache(2, 1 << 26)
+    k.tensor_scale = 4.0
+    assert attention(cache_k=k, scale=1e38) == L.CSA_ERR_INVALID_ARG
+    assert attention(cache_k=k, scale=-1e38) == L.CSA_ERR_INVALID_ARG
+    assert attention(cache_k=k, scale=1e37) == L.CSA_ERR_CUDA
+    v = cache(2, 1 << 27)
+    v.tensor_scale = 1e38
+    assert append(v) == append(k, v) == L.CSA_ERR_INVALID_ARG
+    assert attention(cache_v=v) == append(k) == L.CSA_ERR_CUDA
