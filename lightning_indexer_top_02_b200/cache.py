@@ -276,6 +276,8 @@ def _launch(t, stream):
         if dev == torch.cuda.current_device():
             return torch._C._cuda_getCurrentRawStream(dev), _HERE
         stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream must be on the tensors' device, {dev}")
     return stream.cuda_stream, _elsewhere(dev, stream)
 
 

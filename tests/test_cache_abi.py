@@ -260,3 +260,14 @@ def test_binding_refuses_sizes_past_32_bits():
                  lambda: L.rope_frequencies(64, scaling="yarn", factor=2.0, original_len=2 ** 32 + 4096)):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    """Its device would become the current one, where the tensors' addresses mean nothing."""
+    from types import SimpleNamespace as Fake
+
+    t = Fake(get_device=lambda: 0)
+    handle, _ = C._launch(t, Fake(device_index=0, cuda_stream=5))
+    assert handle == 5
+    with pytest.raises(ValueError, match="stream"):
+        C._launch(t, Fake(device_index=1, cuda_stream=5))
