@@ -36,7 +36,8 @@ bool pick_64(int dv, CattnPlan *pl);
 bool pick_128(int dv, CattnPlan *pl);
 bool pick_192(int dv, CattnPlan *pl);
 bool pick_256(int dv, CattnPlan *pl);
-// The unit's device error word (ptx.cuh), cleared when it holds an error; false: a CUDA call failed.
+// The unit's device error word (ptx.cuh; h is left as it was while no call has used the unit), cleared
+// when it holds an error; false: a CUDA call failed.
 bool error_64(int (&h)[4]);
 bool error_128(int (&h)[4]);
 bool error_192(int (&h)[4]);

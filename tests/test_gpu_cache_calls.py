@@ -135,3 +135,38 @@ def test_writes_are_seen_by_autograd(lib):
     with torch.inference_mode():
         t = torch.zeros((1, 3, 1, 64), dtype=torch.bfloat16, device="cuda")
         L.rotary(t, pos, freq, out=t)                    # (no version to count)
+
+
+# ---------------------------------------------------------------- costs
+
+_ERROR_WORD_SCRIPT = r"""
+import sys
+sys.path.insert(0, {root!r}); sys.path.insert(0, {here!r})
+import torch, lightning_indexer_top_02_b200 as L
+from torch.profiler import profile, ProfilerActivity
+
+def copies():
+    torch.cuda.synchronize()
+    with profile(activities=[ProfilerActivity.CPU, ProfilerActivity.CUDA]) as p:
+        assert L.csa_last_device_error(None) == L.CSA_OK
+        torch.cuda.synchronize()
+    return sum(e.count for e in p.key_averages() if "DtoH" in e.key)
+
+q = torch.randn((1, 4, 16, 128), device="cuda").to(torch.bfloat16)
+k = torch.randn((1, 300, 128), device="cuda").to(torch.bfloat16)
+L.indexer_topk(q, torch.randn((1, 4, 16), device="cuda"), k, m=1, topk=16)
+assert L.csa_last_device_error(None) == L.CSA_OK
+print("indexer alone:", copies())
+assert copies() == 1
+c = L.make_cache("e2m1", 4, 16, 1, 128, device="cuda")
+table = torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+L.cache_attention(q[:, :1], c, c, table, torch.tensor([60], dtype=torch.int32, device="cuda"), scale=0.1)
+print("with attention:", copies())
+assert copies() == 2
+print("script ok")
+"""
+
+
+def test_error_word_costs_what_has_run(lib):
+    """csa_last_device_error copies the words of the units that a call has used, the indexer's alone to begin with."""
+    run_script(_ERROR_WORD_SCRIPT)
