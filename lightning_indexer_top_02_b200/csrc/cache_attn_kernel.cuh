@@ -71,6 +71,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr float kHead = 7.0f;               // a row's reference: its maximum / 2^kHead when it was last raised
 constexpr float kLag = 13.0f;               // and it is raised when a weight would pass 2^kLag (f16: below 2^16)
 constexpr int kNoKey = 0x7FFFFFFF;          // a position no query sees
+constexpr int kStatic = 128;                // static shared memory of a block, at most
 
 struct AttnParams {
     const __nv_bfloat16 *q;                 // [B, S, HA, Dk]
@@ -318,8 +319,13 @@ struct Shape {
     static constexpr int kJoin = kWarps * kRows * (kDv + 2) * 4, kStaging = kWarps * kStages * kStage;
     static constexpr int kBars = kJoin > kStaging ? kJoin : kStaging;    // barriers, abort flag
     static constexpr int kSmem = kBars + kWarps * kStages * 8 + 16;
-    // blocks an SM holds: registers for O and the query, shared memory for the staging
-    static constexpr int kCtas = kNT == 1 && kDk + kDv <= 384 ? 3 : 2;
+    // blocks an SM holds: as many as its 228 KB take beside a block's own kilobyte and static words
+    // (three up to widths of 320 together, two beyond), at most those whose O and query find registers.
+    // (Shares for one CTA more than the SMs hold run in a second round: 8 sequences of 16,384 keys, 8 cache
+    // heads of 192 + 192, take 92 us with three planned and 66 with two.)
+    static constexpr int kHeld = 233472 / (kSmem + 1024 + kStatic);
+    static constexpr int kCtas = kHeld < (kNT == 1 ? 3 : 2) ? kHeld : (kNT == 1 ? 3 : 2);
+    static_assert(kCtas >= 1, "a block fits an SM");
 };
 
 // The kernel that joins the pieces may take the SMs' free places from here on.
@@ -412,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
     extern __shared__ __align__(16) uint8_t smem_raw[];  // staging, then [warp][row][Dv + 2]
     __shared__ long long scratch[kWarps];
     __shared__ Found found;
+    static_assert(sizeof(scratch) + sizeof(found) <= kStatic, "kStatic");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem_raw + Sh::kBars) + warp * kStages;

@@ -170,3 +170,26 @@ print("script ok")
 def test_error_word_costs_what_has_run(lib):
     """csa_last_device_error copies the words of the units that a call has used, the indexer's alone to begin with."""
     run_script(_ERROR_WORD_SCRIPT)
+
+
+@pytest.mark.parametrize("HA", [8, 16])
+@pytest.mark.parametrize("Dv", [64, 128, 192, 256])
+@pytest.mark.parametrize("Dk", [64, 128, 192, 256])
+def test_attention_shares_fit_the_sms(lib, Dk, Dv, HA):
+    """The chunks are shared among CTAs that the GPU holds at a time: their staging (blocks of 64 keys twice, of
+    32 keys three times where rows are wide, four warps) fits in the SMs' shared memory."""
+    L = lib
+    a = L.cache.CsaCacheAttnArgs()
+    for c, D in ((a.cache_k, Dk), (a.cache_v, Dv)):
+        c.data, c.scale, c.dtype, c.H, c.D = 4096, 4096, L.cache.CSA_CACHE_E2M1, 1, D
+        c.num_pages, c.page_size, c.tensor_scale = 1, 1 << 24, 1.0
+    a.q, a.out, a.kv_len, a.page_table = 4096, 1 << 20, 4096, 4096
+    a.max_pages = a.table_stride = 1
+    a.B, a.S, a.HA, a.causal, a.scale = 1, 1, HA, 1, 0.1
+    size = L.csa_cache_attention_workspace_size(a)
+    props = torch.cuda.get_device_properties(0)
+    per_sm, rest = divmod(size, 2 * props.multi_processor_count * HA * (Dv + 2) * 4)
+    assert rest == 0 and per_sm >= 1
+    block = 64 if Dk + Dv <= 256 else 32
+    staging = 4 * (2 if block == 64 else 3) * block * (Dk + Dv) * 9 // 16
+    assert per_sm * (staging + 1024) <= props.shared_memory_per_multiprocessor
