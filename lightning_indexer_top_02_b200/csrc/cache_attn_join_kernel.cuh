@@ -18,7 +18,7 @@ __device__ __forceinline__ void after_kernel_before() { asm volatile("griddepcon
 __global__ void __launch_bounds__(kThreads) cache_attn_pieces_kernel(const AttnParams p, int Dv, int tile_rows)
 {
     __shared__ long long scratch[kWarps];
-    __shared__ float part[kWarps][256 + 2];
+    __shared__ float2 part[kWarps][128 + 1];             // a warp's O, then its maximum and sum
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.x;
     const int all = chunks_of(p, b);
@@ -45,9 +45,9 @@ __global__ void __launch_bounds__(kThreads) cache_attn_pieces_kernel(const AttnP
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         __syncthreads();                                 // (the row before has been read)
         if (lane == 0)
-            part[warp][256] = top;
+            part[warp][128].x = top;
         __syncthreads();
-        top = fmaxf(fmaxf(part[0][256], part[1][256]), fmaxf(part[2][256], part[3][256]));
+        top = fmaxf(fmaxf(part[0][128].x, part[1][128].x), fmaxf(part[2][128].x, part[3][128].x));
         const float base = top == -INFINITY ? 0.0f : top;
         float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
 #pragma unroll 4
@@ -67,17 +67,17 @@ __global__ void __launch_bounds__(kThreads) cache_attn_pieces_kernel(const AttnP
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (64 * j < Dv)
-                *reinterpret_cast<float2 *>(&part[warp][64 * j + 2 * lane]) = make_float2(x[2 * j], x[2 * j + 1]);
+                part[warp][32 * j + lane] = make_float2(x[2 * j], x[2 * j + 1]);
         if (lane == 0)
-            part[warp][257] = sum;
+            part[warp][128].y = sum;
         __syncthreads();
-        sum = part[0][257] + part[1][257] + part[2][257] + part[3][257];
+        sum = part[0][128].y + part[1][128].y + part[2][128].y + part[3][128].y;
         const float inv = sum > 0.0f ? p.v_scale / sum : 0.0f;
         const long long out_row = static_cast<long long>(b) * p.S * p.HA + row;
-        for (int d = 2 * threadIdx.x; d < Dv; d += 2 * kThreads) {
-            const float u = part[0][d] + part[1][d] + part[2][d] + part[3][d];
-            const float v = part[0][d + 1] + part[1][d + 1] + part[2][d + 1] + part[3][d + 1];
-            *reinterpret_cast<uint32_t *>(p.out + out_row * Dv + d) = cache::bf16x2_of(u * inv, v * inv);
+        for (int d = threadIdx.x; d < Dv / 2; d += kThreads) {
+            const float u = part[0][d].x + part[1][d].x + part[2][d].x + part[3][d].x;
+            const float v = part[0][d].y + part[1][d].y + part[2][d].y + part[3][d].y;
+            *reinterpret_cast<uint32_t *>(p.out + out_row * Dv + 2 * d) = cache::bf16x2_of(u * inv, v * inv);
         }
         if (p.lse && threadIdx.x == 0)
             p.lse[out_row] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
