@@ -241,7 +241,7 @@ bool rotary_fits(const csa_rotary_args_t *a, int v)
 
 extern "C" csa_status_t csa_rotary(const csa_rotary_args_t *args, cudaStream_t stream)
 {
-    NvtxRange range("csa_rotary");
+    EntryRange range("csa_rotary");
     const csa_rotary_args_t *a = args;
     if (!a || a->N < 0 || a->H <= 0 || a->D <= 0 || a->dtype < CSA_ELEM_BF16 || a->dtype > CSA_ELEM_FP32 ||
         a->rot_dim < 2 || a->rot_dim % 2 != 0 || a->rot_offset < 0 || a->rot_offset % 2 != 0 ||
@@ -350,7 +350,7 @@ void launch_append(const csa::cache::AppendParams &p, bool inter, unsigned grid,
 
 extern "C" csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStream_t stream)
 {
-    NvtxRange range("csa_cache_append");
+    EntryRange range("csa_cache_append");
     const csa_append_args_t *a = args;
     if (!a || a->N < 0 || a->B < 0 || (!a->cu_tokens && (a->S < 0 || a->N != static_cast<long long>(a->B) * a->S)))
         return CSA_ERR_INVALID_ARG;
@@ -452,7 +452,7 @@ extern "C" csa_status_t csa_cache_append(const csa_append_args_t *args, cudaStre
 
 extern "C" csa_status_t csa_cache_read(const csa_cache_read_args_t *args, cudaStream_t stream)
 {
-    NvtxRange range("csa_cache_read");
+    EntryRange range("csa_cache_read");
     const csa_cache_read_args_t *a = args;
     if (!a || a->B < 0 || a->T < 0)
         return CSA_ERR_INVALID_ARG;
@@ -698,7 +698,7 @@ extern "C" size_t csa_cache_attention_workspace_size(const csa_cache_attn_args_t
 extern "C" csa_status_t csa_cache_attention(const csa_cache_attn_args_t *args, void *workspace,
                                             size_t workspace_bytes, cudaStream_t stream)
 {
-    NvtxRange range("csa_cache_attention");
+    EntryRange range("csa_cache_attention");
     const csa_cache_attn_args_t *a = args;
     csa_status_t st = validate_cattn(a);
     if (st != CSA_OK)

@@ -39,6 +39,13 @@ struct NvtxRange {
     NvtxRange &operator=(const NvtxRange &) = delete;
 };
 
+// An entry point's range.  A CUDA call that failed within it is reported by the entry's status
+// and must not reach the launch checks of the calls after it, which read the last error.
+struct EntryRange : NvtxRange {
+    using NvtxRange::NvtxRange;
+    ~EntryRange() { (void)cudaGetLastError(); }
+};
+
 // Measurement hook: events recorded around this thread's launches.
 thread_local cudaEvent_t *t_events = nullptr;
 thread_local int t_n_events = 0;
@@ -535,7 +542,7 @@ csa_status_t csa_indexer_plan(const csa_args_t *args, csa_plan_t *out)
 csa_status_t csa_indexer_topk_ex(const csa_args_t *args, void *workspace, size_t workspace_bytes,
                                  cudaStream_t stream)
 {
-    NvtxRange range("csa_indexer_topk_ex");
+    EntryRange range("csa_indexer_topk_ex");
     csa_status_t st = validate(args);
     if (st != CSA_OK)
         return st;
@@ -694,7 +701,7 @@ __global__ void zero_kernel(float *x, long long n)
 
 extern "C" csa_status_t csa_sparse_attention(const csa_attn_args_t *args, cudaStream_t stream)
 {
-    NvtxRange range("csa_sparse_attention");
+    EntryRange range("csa_sparse_attention");
     const csa_status_t st = validate_attn(args);
     if (st != CSA_OK)
         return st;
@@ -852,7 +859,7 @@ extern "C" csa_status_t csa_merge_topk(const int32_t *const *idx, const float *c
                                        void *workspace, size_t workspace_bytes,
                                        cudaStream_t stream)
 {
-    NvtxRange range("csa_merge_topk");
+    EntryRange range("csa_merge_topk");
     if (!idx || !score || !key_offset || n_lists < 1 || n_lists > csa::kSelMaxSplits ||
         rows < 0 || k_in < 1 || topk < 1)
         return CSA_ERR_INVALID_ARG;
@@ -940,7 +947,7 @@ extern "C" csa_status_t csa_union_selections(const int32_t *const *lists, int n_
                                              int topk, int T, int cap, int32_t *out,
                                              int32_t *count, cudaStream_t stream)
 {
-    NvtxRange range("csa_union_selections");
+    EntryRange range("csa_union_selections");
     using csa::uni::UnionParams;
     if (rows < 0 || topk <= 0 || T < 0 || cap <= 0 || n_lists < 1 ||
         n_lists > csa::uni::kMaxLists || !lists)
@@ -1022,7 +1029,7 @@ csa_status_t noalloc_scratch(void **out)
 
 extern "C" csa_status_t csa_indexer_topk_noalloc(const csa_args_t *args, cudaStream_t stream)
 {
-    NvtxRange range("csa_indexer_topk_noalloc");
+    EntryRange range("csa_indexer_topk_noalloc");
     csa_status_t st = validate(args);
     if (st != CSA_OK)
         return st;

@@ -193,3 +193,47 @@ def test_attention_shares_fit_the_sms(lib, Dk, Dv, HA):
     block = 64 if Dk + Dv <= 256 else 32
     staging = 4 * (2 if block == 64 else 3) * block * (Dk + Dv) * 9 // 16
     assert per_sm * (staging + 1024) <= props.shared_memory_per_multiprocessor
+
+
+# ---------------------------------------------------------------- errors
+
+_FAILED_CALL_SCRIPT = r"""
+import sys
+sys.path.insert(0, {root!r})
+import torch, lightning_indexer_top_02_b200 as L
+C = L.cache
+c = L.make_cache("e2m1", 64, 64, 1, 128, device="cuda")
+table = torch.arange(64, dtype=torch.int32, device="cuda").view(1, 64)
+lens = torch.tensor([4000], dtype=torch.int32, device="cuda")
+q, out = (torch.zeros((1, 1, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in (0, 1))
+back = torch.empty((1, 100, 1, 128), dtype=torch.bfloat16, device="cuda")
+s = C._cache_struct("c", c)
+pages = (lens.data_ptr(), table.data_ptr(), 64, 64)
+attend = C.CsaCacheAttnArgs(q.data_ptr(), s, s, *pages, None, 0, 1, 1, 8, 1, 0.1, out.data_ptr(), None)
+read = C.CsaCacheReadArgs(s, *pages, 1, 100, back.data_ptr())
+assert L.csa_cache_attention(attend, None, 0, None) == L.CSA_OK
+torch.cuda.synchronize()
+side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+with torch.cuda.stream(side):
+    graph.capture_begin(capture_error_mode="thread_local")
+    try:
+        side.synchronize()                  # not allowed while capturing: the capture is void from here on
+    except RuntimeError as e:
+        print("void:", str(e).splitlines()[0])
+    status = L.csa_cache_attention(attend, None, 0, side.cuda_stream)
+    try:
+        graph.capture_end()
+    except RuntimeError:
+        pass
+print("in the void capture:", status)
+assert status == L.CSA_ERR_CUDA
+assert L.csa_cache_read(read, None) == L.CSA_OK
+torch.cuda.synchronize()
+assert (back == 0).all()
+print("script ok")
+"""
+
+
+def test_a_failed_call_leaves_no_error_behind(lib):
+    """A workspace that cannot be allocated is that call's error, not the next one's."""
+    run_script(_FAILED_CALL_SCRIPT)
