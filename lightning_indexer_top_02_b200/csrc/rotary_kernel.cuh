@@ -158,10 +158,14 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p)
         if (!ready) {
             for (int i = threadIdx.x; i < nt * p.half; i += kThreads) {
                 const int t = static_cast<int>(p.div_half.div(i)), f = i - t * p.half;
+                // the angle's fp32 value, and (to first order) what its rounding leaves out, in radians:
+                // that is up to 9.4e-8, more than sincospif's own error
+                const double h = cache::half_turns(__ldg(p.positions + n0 + t), __ldg(p.inv_freq + f));
+                const float near = static_cast<float>(h), rest = static_cast<float>(h - near) * 3.14159265f;
                 float s, c;
-                sincospif(static_cast<float>(cache::half_turns(__ldg(p.positions + n0 + t), __ldg(p.inv_freq + f))),
-                          &s, &c);
-                cs[i] = make_float2(c * p.scale, (p.inverse ? -s : s) * p.scale);
+                sincospif(near, &s, &c);
+                const float s1 = fmaf(c, rest, s), c1 = fmaf(-s, rest, c);
+                cs[i] = make_float2(c1 * p.scale, (p.inverse ? -s1 : s1) * p.scale);
             }
             __syncthreads();
             ready = true;

@@ -176,3 +176,19 @@ def test_append_far_positions(lib, inter):
     u, w = a * c - b * s, b * c + a * s
     want = torch.stack((u, w), -1).flatten(-2) if inter else torch.cat((u, w), -1)
     assert torch.equal(cache.data[0].transpose(0, 1), want.float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("far", [100, 1_000_000, 2 ** 31 - 1])
+def test_rotary_angles_to_the_last_bit(lib, far):
+    """cos and sin to one step of sincospi (5.97e-8) and of the sum that corrects it (half a step: 2.98e-8); the
+    angle's own rounding to fp32, 9.4e-8 by itself, is put back."""
+    L = lib
+    g = torch.Generator().manual_seed(far % 1000)
+    freq, _ = L.rope_frequencies(64, device="cuda")
+    pos = torch.randint(0, far, (400,), generator=g, dtype=torch.int64).to(torch.int32).cuda()
+    x = torch.zeros((400, 1, 64), device="cuda")
+    x[..., :32] = 1.0
+    got = L.rotary(x, pos, freq)[:, 0].double()
+    c, s = exact_cos_sin(pos, freq.cpu())
+    no_device_error(L)
+    assert max((got[:, :32] - c).abs().max(), (got[:, 32:] - s).abs().max()) <= 8.95e-8
