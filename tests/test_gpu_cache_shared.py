@@ -124,3 +124,26 @@ def test_more_sequences_than_ctas(lib, monkeypatch, HA):
     shared(lib, monkeypatch)
     lens = [(37 * i * i) % 1400 for i in range(300)]
     T.check_attention(lib, B=len(lens), S=1, HA=HA, H=1, Dk=64, Dv=64, page=24, lens=lens, seed=HA)
+
+
+@pytest.mark.parametrize("HA,H", [(8, 1), (16, 2), (64, 1), (128, 1)])
+@pytest.mark.parametrize("topk", [40, 1500])
+def test_selected_without_causality(lib, HA, H, topk):
+    """causal=False: every listed key of the sequence, whatever the query's place."""
+    T.check_attention(lib, B=3, S=3, HA=HA, H=H, Dk=128, Dv=64, page=16, lens=[2000, 2, 0], topk=topk, causal=False, seed=HA + topk)
+
+
+@pytest.mark.parametrize("HA", [8, 16, 64, 128])
+@pytest.mark.parametrize("page,pages", [(16, 20), (64, 40), (24, 100)])
+def test_sequences_longer_than_their_table(lib, HA, page, pages):
+    """kv_len past the pages that the table lists: as many positions as it reaches."""
+    L, g, n = lib, T.gen(page), page * pages
+    c = T.random_cache(L, "e2m1", 2 * pages, page, 1, 128, g)
+    table = T.pages_of(2, pages, 2 * pages, g)
+    q = torch.randn((2, 1, HA, 128), generator=g, device="cuda").to(torch.bfloat16)
+    call = lambda lens: L.cache_attention(q, c, c, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), scale=0.09,  # noqa: E731
+                                          return_lse=True)
+    for long in (n + 1, 10 ** 6, 2 ** 31 - 1):
+        for x, y in zip(call([long, 77]), call([n, 77])):
+            assert torch.equal(x, y)
+    no_device_error(L)
