@@ -8,9 +8,9 @@
 //   O^T [16 dims x 8 rows] += V^T [16 x 16 keys] . P^T [16 keys x 8]
 // With at most 16 rows the work is bound by reading the cache (9/16 byte an
 // element against 4 rows' flops an element), so what matters is how few
-// instructions stand between a code and its use.  A warp takes blocks of 64 (32) keys;
-// their codes and scales come by cp.async two blocks ahead into the warp's own
-// staging rows and go from there into registers in the layout of the MMA's A
+// instructions stand between a code and its use.  A warp takes blocks of 64 keys (32 where
+// a key and a value have more than 256 elements together); their codes and scales come one block
+// ahead (two ahead) into the warp's own staging rows and go from there into registers in the layout of the MMA's A
 // operand: no transposition, and no barrier between warps.
 //   K: the contraction's order is free, so thread (g, t) of a warp takes the
 //     16 * NG consecutive elements 16 * NG * t.. of the rows of its two keys --
@@ -30,8 +30,10 @@
 // P is f16 (11 bits), relative to a reference 2^7 below the running maximum: the row's
 // largest is 2^7 at first and 2^13 at most where the maximum lags, so that half of f16's
 // smallest step is at most 2^-32 of the largest weight (relative to the maximum itself it would
-// be 2^-25, and what 2^17 keys that far below one leave would be lost).  Sums, maxima and O are
-// fp32.
+// be 2^-25, and what 2^17 keys that far below one leave would be lost).  P's 11 bits move one
+// bf16 output in ten by its last bit (relative difference 8.5e-4 to fp32 probabilities, distance
+// from 64-bit values 1.670e-3 instead of 1.658e-3); more would take a second P . V.  Sums,
+// maxima and O are fp32.
 //
 // Tensor-core work here is mma.sync on purpose: tcgen05 reads operands from
 // shared memory, where writing the converted tile and reading it back would
@@ -39,15 +41,21 @@
 // shared memory's 128 bytes a clock allow at the memory's rate.
 //
 // Where every key is read and pages hold whole tiles of 16 keys (kBulk), a tile is
-// 16 rows of one page, and eight lanes fetch a block's eight pieces with one bulk
-// copy each; else every row is found by itself and copied 16 bytes at a time, which
-// takes about 150 instructions more of some 750 a block.
+// 16 rows of one page, and a lane for each of a tile's four arrays (16 lanes a block of 64
+// keys, 8 one of 32) fetches it with one bulk copy; else every row is found by itself and
+// copied 16 bytes at a time.  Instructions are the same within 1 % (21.7 and 21.9 million at
+// 8 sequences x 16,384 keys x 8 cache heads of 128).  Time there, bulk / row by row: 128+128
+// 46.6 / 45.1 us, 192+128 55.3 / 57.7, 192+192 66.6 / 76.9, 128+256 66.0 / 65.3; 32 ragged
+// sequences (below) 155 / 151; one of 777 keys 10.7 / 10.1.  So the bulk copies pay where
+// rows have 192 elements (six pieces, staged without a conflict-free place) and cost up to
+// 5 % elsewhere.
 //
 // Measured at 32 sequences of 512 .. 32,768 keys, 64 heads over 8, D = 128 (615 MB of
-// cache): 151 us, 4.1 TB/s.  Memory alone (the arithmetic left out) takes 111 us, the
-// arithmetic alone 115: 617 instructions for 32 keys, of which 256 are the conversions
-// (64 + 64 of codes, 64 + 64 multiplications by scales, both on half-rate pipes).  12 warps an
-// SM; 8 or 16 warps, deeper staging or shorter blocks were slower (150 -> 158 .. 188 us).
+// cache): 155 us, 4.0 TB/s.  Memory alone (the arithmetic left out) takes 111 us, the
+// arithmetic alone 115: some 1,330 instructions a block of 64 keys with everything around it,
+// of which 512 are the conversions (128 + 128 of codes, 128 + 128 multiplications by scales, both
+// on half-rate pipes).  12 warps an SM; 8 or 16 warps, deeper staging or shorter blocks were
+// slower (150 -> 158 .. 188 us).
 //
 // The CTAs that the GPU holds share out all the chunks (256 or 128 keys) of all row tiles,
 // evenly and in order, whatever the sequences' lengths: a CTA's share is a run of

@@ -30,8 +30,8 @@
 // Waits are bounded (ptx.cuh).
 //
 // Measured at D = 128: a tile of 128 keys takes 2.2 us with 64 rows (a prompt chunk of
-// 1,024 queries x 64 heads over 2,048 selected keys: 230 us, 299 TFLOP/s), 2.4 us with 128 rows
-// (32 sequences x 128 heads over 2,048 keys: 25 us, of which about 11 are the start and
+// 1,024 queries x 64 heads over 2,048 selected keys: 231 us, 298 TFLOP/s), 2.4 us with 128 rows
+// (32 sequences x 128 heads over 2,048 keys: 26 us, of which about 11 are the start and
 // end of an item and 4 the join).  The tensor cores are busy 26 % of the time and the
 // issue slots 44 %: the tile's chain of waits bounds it.  Leaving out the loads and
 // conversions, the softmax or the MMAs takes only 10 to 20 % off.  Tried and slower: two CTAs an

@@ -9,8 +9,8 @@
 namespace csa {
 namespace cache {
 
-// n / d for 0 <= n < 2^31 by one multiplication (d >= 1 fixed on the host):
-// with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, the quotient is
+// n / d for 0 <= n < 2^31 by one multiplication (d >= 1 fixed on the host), after Granlund and
+// Montgomery, "Division by invariant integers using multiplication" (1994): with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, the quotient is
 // (mulhi(m, n) + n) >> l.
 struct FastDiv {
     uint32_t d, m, l;

@@ -565,6 +565,18 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
         return CSA_ERR_CUDA;
     const int H = a->cache_k.H, G = a->HA / H;
     pl->rows = a->idx ? G : a->S * G;
+    // The tensor-memory kernel takes what does not fit one tile of the register kernel, which reads and
+    // converts every key once for 16 rows.  Wide / register (as tiles of 16), us, D = 128, by rows:
+    //                                            17-20        32         48         64        128
+    //   16 x 16,384 keys, 8 cache heads        228 / 181   230 / 189  232 / 274  225 / 356  280 / 688
+    //   the same, ragged                       228 / 118   226 / 127  228 / 181  224 / 235  262 / 451
+    //   4 x 4,096 keys, 2 cache heads         18.2 / 14.7 18.9 / 16.1 20.1 / 19.0 20.9 / 22.9 22.7 / 29.1
+    //   32 x 2,048 keys, 1 cache head         19.3 / 21.4 20.2 / 22.9 21.5 / 27.4 21.8 / 31.2 23.7 / 46.3
+    //   32 x 2,048 selected                   19.0 / 23.0 19.9 / 24.3 20.9 / 30.5 21.8 / 35.0 23.6 / 51.0
+    //   512 queries over 2,048 selected        128 / 127   131 / 139  133 / 197  136 / 248  168 / 475
+    // For selections the border is where it should be; dense calls over long contexts would gain from a
+    // higher one (32 rows, ragged 48), for the wide kernel's shares are even in the table's reach, not
+    // in the sequences' keys.
     pl->wide = pl->rows > 16;
     const CacheView ck = cache_view(a->cache_k), cv = cache_view(a->cache_v);
     pl->bulk = !a->idx && a->cache_k.page_size % 16 == 0 && ck.scale_stride % 16 == 0 && cv.scale_stride % 16 == 0;
@@ -595,10 +607,14 @@ csa_status_t plan_cattn(const csa_cache_attn_args_t *a, CattnPlan *pl)
             }
         }
     } else {
-        // as many CTAs as the GPU holds share the chunks; where no tile has more
-        // than kAlone chunks, a CTA each, and no second kernel (one sequence of 777 keys, 8
-        // heads: 10.7 us on the device alone, 9.7 shared and joined, but 17 and 21 as issued;
-        // 16 such: 11.0 and 17.1)
+        // as many CTAs as the GPU holds share the chunks; where no tile has more than kAlone
+        // chunks (256 keys each at D = 128), a CTA each, and no second kernel.  Alone / shared and joined,
+        // us on the device, 32 heads over 8, by keys:
+        //                    256         512         777        1,024
+        //   1 sequence    5.5 / 8.4   7.8 / 9.7   10.9 / 9.8  11.1 / 9.8
+        //   16 sequences  5.8 / 9.4   7.8 / 10.8  11.0 / 16.9 11.2 / 17.1
+        // and 17 / 21 us issued one by one, at each of them: the second launch costs more than the 1.3
+        // us that a captured step of one sequence would gain at three or four chunks.
         constexpr long long kAlone = 4;
         const long long chunks = (most + pl->chunk - 1) / pl->chunk;
         const long long held = static_cast<long long>(sms) * pl->ctas;

@@ -5,11 +5,11 @@
 // lanes of 16 elements each -- one E2M1 scale group, 32 bytes of bf16 -- in a
 // group of 2^n lanes, which exchange only the row maximum that the E4M3 scale needs.
 // A lane moves whole 32-byte sectors (two 16-byte stores at a stride of 32 write half
-// sectors: 19.3 us instead of 15.6 for the 4-bit read below).  Measured: 18 thousand ragged tokens x
-// 8 heads of 128 + 128 bf16, every key element rotated, 43 us (4.1 TB/s; the rotation
-// carried in 40 bits is about 300 instructions for 16 elements, and it is what bounds the
-// append: left out, an earlier version took 48 us instead of 64); 8 x 32,768 rows of
-// 128 from 4 bits to bf16 13.9 us (5.8 TB/s).
+// sectors: 19.3 us instead of 15.6 for the 4-bit read below, in L2).  Measured, on inputs that do not
+// stand in L2: 18 thousand ragged tokens x 8 heads of 128 + 128 bf16, every key element
+// rotated, 46 us (3.9 TB/s; the rotation carried in 40 bits is about 300 instructions for 16
+// elements, and it is what bounds the append: left out, an earlier version took 48 us instead
+// of 64); 8 x 32,768 rows of 128 from 4 bits to bf16 17.0 us (4.8 TB/s).
 #pragma once
 #include "cache_common.cuh"
 #include "ptx.cuh"

@@ -9,9 +9,8 @@
 // sincospi a token and no table is read from memory.  What it took to reach memory's
 // rate was instructions: packed conversions, one shape for rotated and copied pieces
 // (a warp's accesses do not diverge) and kAhead units loaded before the angles are
-// waited for.  8,192 tokens x 64 heads of 128 bf16 (64 rotated, interleaved): 43 us,
-// 6.2 TB/s, where a plain elementwise pass over the same tensors takes 41; 4,099 x 16 x 192
-// fp32: 15.6 us, 6.4 TB/s.
+// waited for.  8,192 tokens x 64 heads of 128 bf16 (64 rotated, interleaved): 45 us,
+// 5.9 TB/s; 4,099 x 16 x 192 fp32: 18.4 us, 5.5 TB/s (inputs that do not stand in L2).
 #pragma once
 #include "cache_common.cuh"
 
