@@ -8,7 +8,9 @@
  * and never synchronises.  Kernels run on the current device, which the
  * pointers must belong to.  Floating-point inputs must be finite (other
  * values give unspecified but memory-safe results), except where a row is
- * masked: what lies in a cache outside a sequence's rows is never used.
+ * masked: what lies in a cache outside a sequence's rows is never used.  Lengths, page
+ * tables and lists must not change while a call's work runs (results are then
+ * unspecified, the access stays within the caches and outputs).
  *
  * The cache.  A page holds page_size rows for each of H heads, head by head:
  * row o of head h in page p starts at

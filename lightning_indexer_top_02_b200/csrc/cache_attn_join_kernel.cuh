@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(kThreads) cache_attn_pieces_kernel(const AttnP
         const int k0 = cta_of(start, total, ctas), k1 = cta_of(start + all - 1, total, ctas);
         if (k0 == k1)
             continue;                                    // one CTA had the whole tile
+        if (k0 < 0 || k1 >= p.ctas)
+            continue;                                    // (lengths that changed meanwhile: no such pieces)
         // the first CTA's piece begins the tile (its second slot), the others' end or fill it
         auto piece = [&](int k) { return (2ll * k + (k == k0 ? 1 : 0)) * tile_rows + r % tile_rows; };
         float top = -INFINITY;

@@ -384,6 +384,8 @@ __device__ __forceinline__ void find_chunk(const AttnParams &p, long long x, Fou
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     long long carry = 0;
+    if (threadIdx.x == 0)
+        *found = Found{0, 0};                            // (lengths that changed meanwhile: x may be nowhere)
     for (int base = 0; base < p.B; base += kThreads) {
         const int b = base + threadIdx.x;
         const long long v = b < p.B ? static_cast<long long>(chunks_of(p, b)) * p.works : 0;
@@ -473,9 +475,11 @@ __global__ void __launch_bounds__(kThreads, Shape<kDk, kDv, kNT>::kCtas)
     while (left > 0) {
         int work = blockIdx.x, lo = 0, hi = p.most, all = p.most;   // the segment: chunks lo .. hi - 1 of `all`
         if (p.ctas) {
-            all = chunks_of(p, seq);
-            if (all <= 0)
-                break;                                   // (the lengths changed meanwhile: not allowed, but no endless loop)
+            // (lengths that change meanwhile are not allowed, but lead neither out of the
+            // batch nor into an endless loop)
+            all = seq < p.B ? chunks_of(p, seq) : 0;
+            if (all <= 0 || y >= static_cast<long long>(all) * p.works)
+                break;
             const int w = static_cast<int>(y / all);
             lo = static_cast<int>(y - static_cast<long long>(w) * all);
             hi = static_cast<int>(min(static_cast<long long>(all), lo + left));
