@@ -177,19 +177,30 @@ def _cache_struct(name: str, c: Cache) -> CsaCache:
                     c.tensor_scale)
 
 
+_autograd = _increment_version = None       # torch.autograd's, from the first call on
+
+
+def _load_autograd():
+    global _autograd, _increment_version
+    from torch.autograd import forward_ad, graph
+
+    _autograd, _increment_version = forward_ad, graph.increment_version
+    return forward_ad
+
+
 def _on(dev, names, *tensors):
     """Every tensor on one CUDA device, and none that would need a gradient or carries a
     tangent.  (Checked in one go, names looked up only for an error: this is on every
     call's path.)"""
-    import torch
-
-    forward_ad = torch.autograd.forward_ad
+    forward_ad = _autograd or _load_autograd()
     for t in tensors:
         if t is not None and (t.get_device() != dev or t.requires_grad):
             break
     else:
         if dev >= 0 and forward_ad._current_level < 0:
             return
+    import torch
+
     for name, t in zip(names.split(), tensors):
         if t is None:
             continue
@@ -212,11 +223,9 @@ def _ints(**sizes):
 
 
 def _wrote(*tensors):
-    """Counts a change of the caller's tensors that a call writes through their
+    """Counts a change of the caller's tensors that a call (past _on) writes through their
     addresses, so that autograd refuses to use a value it had kept of them."""
-    import torch
-
-    torch.autograd.graph.increment_version(tensors)
+    _increment_version(tensors)
 
 
 def _int32(name, t, shape):
@@ -405,8 +414,9 @@ def cache_append(k, cache_k: Cache, page_table, kv_len, *, v=None, cache_v: Opti
         st = L.load_library().csa_cache_append(ctypes.byref(a), s)
     if st:
         raise L.CsaError(st, "csa_cache_append")
-    for c in (cache_k, cache_v) if cache_v is not None else (cache_k,):
-        _wrote(c.data) if c.scale is None else _wrote(c.data, c.scale)
+    _wrote(cache_k.data) if cache_k.scale is None else _wrote(cache_k.data, cache_k.scale)
+    if cache_v is not None:
+        _wrote(cache_v.data) if cache_v.scale is None else _wrote(cache_v.data, cache_v.scale)
 
 
 def cache_read(cache: Cache, page_table, kv_len, T: int, *, out=None, stream=None):
@@ -417,7 +427,8 @@ def cache_read(cache: Cache, page_table, kv_len, T: int, *, out=None, stream=Non
     B, pages = _table(page_table, kv_len)
     c = _cache_struct("cache", cache)
     T = int(T)
-    _ints(T=T)
+    if not -_INT_MAX <= T <= _INT_MAX:
+        _ints(T=T)
     shape = (B, T, c.H, c.D)
     if out is not None and (out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous()):
         raise TypeError(f"out must be a contiguous bfloat16 tensor of shape {shape}")
