@@ -184,7 +184,8 @@ def _load_autograd():
     global _autograd, _increment_version
     from torch.autograd import forward_ad, graph
 
-    _autograd, _increment_version = forward_ad, graph.increment_version
+    _increment_version = graph.increment_version    # before _autograd, which other threads look at
+    _autograd = forward_ad
     return forward_ad
 
 
