@@ -237,3 +237,65 @@ print("script ok")
 def test_a_failed_call_leaves_no_error_behind(lib):
     """A workspace that cannot be allocated is that call's error, not the next one's."""
     run_script(_FAILED_CALL_SCRIPT)
+
+
+# ---------------------------------------------------------------- forms of the arguments
+
+def test_views_as_arguments(lib):
+    """Tables inside wider ones, caches as E4M3 tensors, heads and tokens broadcast: as their plain copies."""
+    import test_gpu_cache as T
+    L, g = lib, T.gen(21)
+    wide = torch.randperm(2 * 40, generator=g, device="cuda")[:80].to(torch.int32).view(2, 40)
+    table = wide[:, 8:32]
+    lens = torch.tensor([380, 100], dtype=torch.int32, device="cuda")
+    kc, vc = (T.random_cache(L, "e2m1", 80, 16, 2, 128, g) for _ in (0, 1))
+    as8 = lambda c: L.Cache(c.dtype, c.data if c.dtype == "e2m1" else c.data.view(torch.float8_e4m3fn),  # noqa: E731
+                            c.scale.view(torch.float8_e4m3fn) if c.dtype == "e2m1" else c.scale, c.tensor_scale)
+    for HA in (16, 64):
+        q = torch.randn((2, 1, HA, 128), generator=g, device="cuda").to(torch.bfloat16)
+        assert torch.equal(L.cache_attention(q, as8(kc), as8(vc), table, lens, scale=0.09),
+                           L.cache_attention(q, kc, vc, table.contiguous(), lens, scale=0.09))
+    row = torch.randn((1, 1, 1, 128), generator=g, device="cuda").to(torch.bfloat16)
+    freq, _ = L.rope_frequencies(64, device="cuda")
+    for kind in ("bf16", "e4m3", "e2m1"):
+        a = T.random_cache(L, kind, 80, 16, 2, 128, g)
+        b = L.Cache(kind, a.data.clone(), None if a.scale is None else a.scale.clone())
+        c8 = as8(a) if kind != "bf16" else a
+        L.cache_append(row.expand(2, 7, 2, 128), c8, table, lens, inv_freq=freq)
+        L.cache_append(row.expand(2, 7, 2, 128).contiguous(), b, table.contiguous(), lens, inv_freq=freq)
+        assert torch.equal(a.data, b.data) and (a.scale is None or torch.equal(a.scale, b.scale))
+        assert torch.equal(L.cache_read(c8, table, lens, 390), L.cache_read(b, table.contiguous(), lens, 390))
+    pos = torch.arange(14, dtype=torch.int32, device="cuda").view(2, 7)
+    assert torch.equal(L.rotary(row.expand(2, 7, 2, 128), pos, freq), L.rotary(row.expand(2, 7, 2, 128).contiguous(), pos, freq))
+    T.no_device_error(L)
+
+
+def test_calls_from_two_threads(lib):
+    """Two host threads, a stream each, at the same time."""
+    import threading
+
+    import test_gpu_cache as T
+    L = lib
+    states = [T.step_state(L, T=200), T.step_state(L, T=777)]
+    want = [T.decode_step(L, s)[0] for s in states]
+    torch.cuda.synchronize()
+    got, failed = [[], []], []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(30):
+                got[i].append(T.decode_step(L, states[i], stream=stream)[0])
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for g, w in zip(got, want):
+        assert len(g) == 30 and all(torch.equal(x, w) for x in g)
+    T.no_device_error(L)
